@@ -12,10 +12,18 @@ to own device memory and streams.
 
 k and v may have fewer heads than q (grouped- or multi-query attention); the
 helpers then call the ``_gqa`` entry points.
+
+Serving over a cache in pages (packed tokens; include/mea_attn.h has the layout):
+
+    q = paged_append(q, k, v, k_cache, v_cache, weights, cu_q, kv_len, page_table, positions, freq)
+    o, lse = attention_paged(q, k_cache, v_cache, cu_q, kv_len, page_table, max_q, max_kv)
+    attention_paged_weights(q, lse, k_cache, weights, cu_q, kv_len, page_table, max_q, max_kv)
+    kept, kv_len = paged_evict(k_cache, v_cache, weights, page_table, kv_len, dst_table, n_keep, n_recent)
 """
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -25,12 +33,16 @@ import torch
 __all__ = [
     "MeaError", "load_library", "library_path",
     "MEA_OK", "MEA_ERR_INVALID_ARG", "MEA_ERR_UNSUPPORTED", "MEA_ERR_MISALIGNED", "MEA_ERR_WORKSPACE",
-    "MEA_ERR_CUDA", "MEA_ERR_TIMEOUT", "MEA_DTYPE_F32", "MEA_DTYPE_BF16",
+    "MEA_ERR_CUDA", "MEA_ERR_TIMEOUT", "MEA_ERR_PAGE", "MEA_DTYPE_F32", "MEA_DTYPE_BF16",
     "MEA_BWD_ALL", "MEA_BWD_PREPROCESS", "MEA_BWD_MAIN", "MEA_BWD_FINALIZE", "MEA_NOALLOC_SCRATCH_BYTES",
     "mea_attn_fwd", "mea_attn_bwd", "mea_attn_bwd_phase", "mea_attn_bwd_workspace_size", "mea_attn_bwd_noalloc",
     "mea_attn_bwd_accum", "mea_attn_bwd_accum_workspace_size", "mea_attn_accum_convert",
     "mea_attn_fwd_gqa", "mea_attn_bwd_gqa", "mea_attn_bwd_gqa_workspace_size", "mea_attn_fwd_fp8",
     "mea_attn_combine", "mea_attn_decode", "mea_attn_decode_workspace_size", "attention_decode",
+    "MEA_ROPE_HALF", "MEA_ROPE_INTERLEAVED", "MEA_ROPE_SCALE_NONE", "MEA_ROPE_SCALE_LINEAR", "MEA_ROPE_SCALE_BASE",
+    "MEA_ROPE_SCALE_BY_PARTS", "mea_rope_frequencies", "mea_rope", "rope", "mea_paged_append", "paged_append",
+    "mea_attn_paged", "mea_attn_paged_workspace_size", "attention_paged", "mea_attn_paged_weights",
+    "attention_paged_weights", "mea_paged_evict", "paged_evict",
     "mea_last_device_error",
     "mea_selftest_bounded_wait", "mea_status_string", "mea_last_error_message", "mea_version", "attention_forward", "attention_backward",
 ]
@@ -42,6 +54,15 @@ MEA_ERR_MISALIGNED = 3
 MEA_ERR_WORKSPACE = 4
 MEA_ERR_CUDA = 5
 MEA_ERR_TIMEOUT = 6
+MEA_ERR_PAGE = 7
+
+MEA_ROPE_HALF = 0
+MEA_ROPE_INTERLEAVED = 1
+
+MEA_ROPE_SCALE_NONE = 0
+MEA_ROPE_SCALE_LINEAR = 1
+MEA_ROPE_SCALE_BASE = 2
+MEA_ROPE_SCALE_BY_PARTS = 3
 
 MEA_DTYPE_F32 = 0
 MEA_DTYPE_BF16 = 1
@@ -112,6 +133,21 @@ def load_library() -> ctypes.CDLL:
     lib.mea_attn_decode_workspace_size.restype = i
     lib.mea_attn_decode.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, i, f, i, vp, sz, vp]
     lib.mea_attn_decode.restype = i
+    ll, d = ctypes.c_longlong, ctypes.c_double
+    lib.mea_rope_frequencies.argtypes = [vp, i, d, i, d, d, d, d]
+    lib.mea_rope_frequencies.restype = i
+    lib.mea_rope.argtypes = [vp] * 4 + [i] * 7 + [f, i, i, vp]
+    lib.mea_rope.restype = i
+    lib.mea_paged_append.argtypes = [vp] * 12 + [i] * 5 + [ll] * 3 + [i] * 5 + [f, i, vp]
+    lib.mea_paged_append.restype = i
+    lib.mea_attn_paged_workspace_size.argtypes = [i] * 8 + [ctypes.POINTER(sz)]
+    lib.mea_attn_paged_workspace_size.restype = i
+    lib.mea_attn_paged.argtypes = [vp] * 8 + [i] * 5 + [ll] + [i] * 5 + [f, i, vp, sz, vp]
+    lib.mea_attn_paged.restype = i
+    lib.mea_attn_paged_weights.argtypes = [vp] * 7 + [i] * 5 + [ll] + [i] * 5 + [f, i, vp]
+    lib.mea_attn_paged_weights.restype = i
+    lib.mea_paged_evict.argtypes = [vp] * 8 + [i] * 9 + [i, vp]
+    lib.mea_paged_evict.restype = i
     lib.mea_selftest_bounded_wait.argtypes = [vp, vp]
     lib.mea_selftest_bounded_wait.restype = i
     lib.mea_last_device_error.argtypes = [vp]
@@ -424,6 +460,281 @@ def attention_decode(q, k, v, scale: float | None = None, stream=None):
     ws = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
     mea_attn_decode(q, k, v, o, lse, scale, ws, stream)
     return o, lse
+
+
+# ------------------------------------- rotary positions and the paged cache
+
+def mea_rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: int = MEA_ROPE_SCALE_NONE, factor: float = 1.0,
+                         original_len: float = 0.0, slow: float = 1.0, fast: float = 32.0) -> torch.Tensor:
+    """C ``mea_rope_frequencies``: the angles per position as an fp64 CPU tensor [rot_dim / 2]."""
+    out = (ctypes.c_double * max(1, int(rot_dim) // 2))()
+    _check(load_library().mea_rope_frequencies(out, int(rot_dim), float(base), int(scaling), float(factor),
+                                               float(original_len), float(slow), float(fast)), "mea_rope_frequencies")
+    return torch.tensor(list(out), dtype=torch.float64)
+
+
+def _bad(where: str, what: str):
+    raise MeaError(MEA_ERR_INVALID_ARG, f"{where}: {what}")
+
+
+def _same_device(where: str, first, named) -> None:
+    """Every tensor on ``first``'s CUDA device; all but the packed ones dense, of the given dtype."""
+    dev = first.device
+    if dev.type != "cuda":
+        _bad(where, "CUDA tensors")
+    for name, t, dtype in named:
+        if t is None:
+            continue
+        if t.device != dev:
+            _bad(where, f"{name} is not on the device of the first tensor")
+        if t.dtype != dtype:
+            _bad(where, f"{name} must be {dtype}")
+        if not t.is_contiguous():
+            _bad(where, f"{name} must be contiguous")
+
+
+def _packed(where: str, name: str, t, dtype, T=None, heads=None, D=None) -> int:
+    """Token stride of packed [T, heads, D] rows: heads and dims dense, any token stride."""
+    if t.dim() != 3 or t.dtype != dtype or (T is not None and t.shape[0] != T) or \
+            (heads is not None and t.shape[1] != heads) or (D is not None and t.shape[2] != D):
+        _bad(where, f"{name} shape/dtype mismatch")
+    n, h, d = t.shape
+    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+        _bad(where, f"{name}: heads and head dims must be dense")
+    return t.stride(0) if n > 1 else h * d
+
+
+def _pages(where: str, k_cache, v_cache=None, weights=None, like=None):
+    """Sizes of a cache [pages, H_kv, page_size, D]; v_cache alike, weights [pages, H_kv, page_size] fp32."""
+    if k_cache.dim() != 4:
+        _bad(where, "k_cache must be [pages, H_kv, page_size, D]")
+    if like is not None and like.dtype != k_cache.dtype:
+        _bad(where, "k_cache dtype mismatch")
+    if v_cache is not None and v_cache.shape != k_cache.shape:
+        _bad(where, "v_cache must be shaped like k_cache")
+    if weights is not None and weights.shape != k_cache.shape[:3]:
+        _bad(where, "weights must be [pages, H_kv, page_size]")
+    return k_cache.shape
+
+
+def _batch(where: str, kv_len, page_table, cu_q=None):
+    if kv_len.dim() != 1 or page_table.dim() != 2 or page_table.shape[0] != kv_len.shape[0]:
+        _bad(where, "kv_len must be [B] and page_table [B, max_pages]")
+    if cu_q is not None and tuple(cu_q.shape) != (kv_len.shape[0] + 1,):
+        _bad(where, "cu_q must be [B + 1]")
+    return page_table.shape
+
+
+def _launch(where: str, fn, device, stream, *args) -> None:
+    """fn(*args, stream) with ``device`` current (its own stream where none is given)."""
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            st = fn(*args, _stream_handle(stream))
+    else:
+        st = fn(*args, _stream_handle(stream))
+    _check(st, where)
+
+
+def _allocating(stream, device):
+    """Context in which outputs and scratch of a call on ``stream`` are allocated: on that stream, so
+    that the allocator does not hand their memory on while the call may still run."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream_handle(stream), device=device)
+    return torch.cuda.stream(stream)
+
+
+def mea_rope(x, y, positions, freq, layout: int = MEA_ROPE_HALF, mscale: float = 1.0, inverse: bool = False,
+             stream=None) -> None:
+    """C ``mea_rope``: y = mscale * R(positions) x on x [B,H,N,D] (y may be x); positions int32 [N] or
+    [B,N]; freq fp64 [rot_dim / 2] on the device; ``inverse`` is the gradient's direction."""
+    B, H, N, D = _shape4(x, "x")
+    if y.shape != x.shape or y.dtype != x.dtype:
+        _bad("mea_rope", "y shape/dtype mismatch")
+    if freq.dim() != 1:
+        _bad("mea_rope", "freq must be [rot_dim / 2]")
+    if tuple(positions.shape) not in ((N,), (B, N)):
+        _bad("mea_rope", "positions must be [N] or [B, N]")
+    _same_device("mea_rope", x, (("x", x, x.dtype), ("y", y, x.dtype), ("positions", positions, torch.int32),
+                                 ("freq", freq, torch.float64)))
+    _launch("mea_rope", load_library().mea_rope, x.device, stream, _ptr(x), _ptr(y), _ptr(positions), _ptr(freq), B, H,
+            N, D, 2 * freq.shape[0], int(positions.dim() == 2), int(layout), float(mscale), int(bool(inverse)),
+            _dtype_code(x))
+
+
+def rope(x, positions, freq, interleaved: bool = False, mscale: float = 1.0, inverse: bool = False, stream=None):
+    """Allocate y with torch and run ``mea_rope``; the gradient of x is ``rope(dy, ..., inverse=True)``."""
+    with _allocating(stream, x.device):
+        y = torch.empty_like(x, memory_format=torch.contiguous_format)
+    mea_rope(x, y, positions, freq, MEA_ROPE_INTERLEAVED if interleaved else MEA_ROPE_HALF, mscale, inverse, stream)
+    return y
+
+
+def mea_paged_append(q, q_out, k, v, k_cache, v_cache, weights, cu_q, kv_len, page_table, positions=None, freq=None,
+                     layout: int = MEA_ROPE_HALF, mscale: float = 1.0, stream=None) -> None:
+    """C ``mea_paged_append``: k turned and v go to the sequences' last slots, q turned to q_out.  q and
+    q_out may be None (keys only), weights None (none kept), positions None (the slots), freq None (no
+    rotation)."""
+    w = "mea_paged_append"
+    pages, Hkv, page, D = _pages(w, k_cache, v_cache, weights)
+    B, max_pages = _batch(w, kv_len, page_table, cu_q)
+    dt = k_cache.dtype
+    ks = _packed(w, "k", k, dt, None, Hkv, D)
+    T = k.shape[0]
+    vs = _packed(w, "v", v, dt, T, Hkv, D)
+    if (q is None) != (q_out is None):
+        _bad(w, "q and q_out go together")
+    H, qs = 0, 0
+    if q is not None:
+        qs, H = _packed(w, "q", q, dt, T, None, D), q.shape[1]
+        if q_out.shape != q.shape:
+            _bad(w, "q_out must be shaped like q")
+    if positions is not None and tuple(positions.shape) != (T,):
+        _bad(w, "positions must be [T]")
+    if freq is not None and freq.dim() != 1:
+        _bad(w, "freq must be [rot_dim / 2]")
+    _same_device(w, k, (("k_cache", k_cache, dt), ("v_cache", v_cache, dt), ("weights", weights, torch.float32),
+                        ("cu_q", cu_q, torch.int32), ("kv_len", kv_len, torch.int32),
+                        ("page_table", page_table, torch.int32), ("positions", positions, torch.int32),
+                        ("freq", freq, torch.float64), ("q_out", q_out, dt)))
+    if v.device != k.device or (q is not None and q.device != k.device):
+        _bad(w, "q, k and v must be on one device")
+    _launch(w, load_library().mea_paged_append, k.device, stream, _ptr(q), _ptr(q_out), _ptr(k), _ptr(v),
+            _ptr(k_cache), _ptr(v_cache), _ptr(weights), _ptr(cu_q), _ptr(kv_len), _ptr(page_table), _ptr(positions),
+            _ptr(freq), T, B, H, Hkv, D, qs, ks, vs, pages, page, max_pages, 0 if freq is None else 2 * freq.shape[0],
+            int(layout), float(mscale), _dtype_code(k_cache))
+
+
+def paged_append(q, k, v, k_cache, v_cache, weights, cu_q, kv_len, page_table, positions=None, freq=None,
+                 interleaved: bool = False, mscale: float = 1.0, stream=None):
+    """Allocate the turned q with torch and run ``mea_paged_append``; returns it (None without q).  Rows
+    outside every sequence are not written."""
+    q_out = None
+    if q is not None:
+        with _allocating(stream, q.device):
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    mea_paged_append(q, q_out, k, v, k_cache, v_cache, weights, cu_q, kv_len, page_table, positions, freq,
+                     MEA_ROPE_INTERLEAVED if interleaved else MEA_ROPE_HALF, mscale, stream)
+    return q_out
+
+
+def mea_attn_paged_workspace_size(T: int, B: int, H: int, H_kv: int, D: int, max_q: int, max_kv: int,
+                                  dtype=torch.bfloat16) -> int:
+    """C ``mea_attn_paged_workspace_size`` (for the current CUDA device)."""
+    out = ctypes.c_size_t(0)
+    code = MEA_DTYPE_BF16 if dtype == torch.bfloat16 else MEA_DTYPE_F32
+    _check(load_library().mea_attn_paged_workspace_size(T, B, H, H_kv, D, max_q, max_kv, code, ctypes.byref(out)),
+           "mea_attn_paged_workspace_size")
+    return int(out.value)
+
+
+def mea_attn_paged(q, k_cache, v_cache, o, lse, cu_q, kv_len, page_table, max_q: int, max_kv: int, scale: float,
+                   workspace, stream=None) -> None:
+    """C ``mea_attn_paged``: q [T,H,D] (any token stride) over the pages; writes o [T,H,D] and lse [T,H]
+    (fp32).  ``workspace`` a CUDA tensor of at least ``mea_attn_paged_workspace_size`` bytes (None when 0)."""
+    w = "mea_attn_paged"
+    pages, Hkv, page, D = _pages(w, k_cache, v_cache, like=q)
+    B, max_pages = _batch(w, kv_len, page_table, cu_q)
+    dt = k_cache.dtype
+    qs = _packed(w, "q", q, dt, None, None, D)
+    T, H = q.shape[:2]
+    if o.shape != q.shape or tuple(lse.shape) != (T, H):
+        _bad(w, "o must be shaped like q, lse [T, H]")
+    _same_device(w, q, (("k_cache", k_cache, dt), ("v_cache", v_cache, dt), ("o", o, dt), ("lse", lse, torch.float32),
+                        ("cu_q", cu_q, torch.int32), ("kv_len", kv_len, torch.int32),
+                        ("page_table", page_table, torch.int32)))
+    ws_bytes = 0
+    if workspace is not None:
+        if workspace.device != q.device or not workspace.is_contiguous():
+            _bad(w, "workspace must be a contiguous tensor on the device")
+        ws_bytes = workspace.numel() * workspace.element_size()
+    _launch(w, load_library().mea_attn_paged, q.device, stream, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(o),
+            _ptr(lse), _ptr(cu_q), _ptr(kv_len), _ptr(page_table), T, B, H, Hkv, D, qs, pages, page, max_pages,
+            int(max_q), int(max_kv), float(scale), _dtype_code(q), _ptr(workspace), ws_bytes)
+
+
+def attention_paged(q, k_cache, v_cache, cu_q, kv_len, page_table, max_q: int, max_kv: int,
+                    scale: float | None = None, stream=None):
+    """Allocate (o, lse) and the workspace with torch and run ``mea_attn_paged``.  Rows outside every
+    sequence are not written."""
+    _pages("attention_paged", k_cache)
+    if q.dim() != 3:
+        _bad("attention_paged", "q must be [T, H, D]")
+    if not q.is_cuda:
+        _bad("attention_paged", "CUDA tensors")
+    if scale is None:
+        scale = 1.0 / math.sqrt(q.shape[-1])
+    T, H, D = q.shape
+    with torch.cuda.device(q.device) if q.device.index != torch.cuda.current_device() else contextlib.nullcontext():
+        n = mea_attn_paged_workspace_size(T, kv_len.shape[0], H, k_cache.shape[1], D, max_q, max_kv, q.dtype)
+    with _allocating(stream, q.device):
+        o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+        ws = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+    mea_attn_paged(q, k_cache, v_cache, o, lse, cu_q, kv_len, page_table, max_q, max_kv, scale, ws, stream)
+    return o, lse
+
+
+def mea_attn_paged_weights(q, lse, k_cache, weights, cu_q, kv_len, page_table, max_q: int, max_kv: int, scale: float,
+                           stream=None) -> None:
+    """C ``mea_attn_paged_weights``: adds to weights [pages,H_kv,page_size] what every cached key's
+    probabilities sum to over the rows of the call (lse [T,H] from ``mea_attn_paged``)."""
+    w = "mea_attn_paged_weights"
+    pages, Hkv, page, D = _pages(w, k_cache, None, weights, q)
+    B, max_pages = _batch(w, kv_len, page_table, cu_q)
+    qs = _packed(w, "q", q, k_cache.dtype, None, None, D)
+    T, H = q.shape[:2]
+    if tuple(lse.shape) != (T, H):
+        _bad(w, "lse must be [T, H]")
+    _same_device(w, q, (("k_cache", k_cache, k_cache.dtype), ("weights", weights, torch.float32),
+                        ("lse", lse, torch.float32), ("cu_q", cu_q, torch.int32), ("kv_len", kv_len, torch.int32),
+                        ("page_table", page_table, torch.int32)))
+    _launch(w, load_library().mea_attn_paged_weights, q.device, stream, _ptr(q), _ptr(lse), _ptr(k_cache),
+            _ptr(weights), _ptr(cu_q), _ptr(kv_len), _ptr(page_table), T, B, H, Hkv, D, qs, pages, page, max_pages,
+            int(max_q), int(max_kv), float(scale), _dtype_code(q))
+
+
+def attention_paged_weights(q, lse, k_cache, weights, cu_q, kv_len, page_table, max_q: int, max_kv: int,
+                            scale: float | None = None, stream=None) -> None:
+    """``mea_attn_paged_weights`` with the scale of ``attention_paged``."""
+    mea_attn_paged_weights(q, lse, k_cache, weights, cu_q, kv_len, page_table, max_q, max_kv,
+                           1.0 / math.sqrt(q.shape[-1]) if scale is None else scale, stream)
+
+
+def mea_paged_evict(k_cache, v_cache, weights, page_table, kv_len, dst_table, kv_len_out, keep_idx, n_recent: int,
+                    stream=None) -> None:
+    """C ``mea_paged_evict``: cuts sequences to keep_idx.shape[2] keys, moved to the pages of dst_table
+    (``page_table`` itself: in place); writes keep_idx [B,H_kv,n_keep] and kv_len_out [B] (int32, or None)."""
+    w = "mea_paged_evict"
+    pages, Hkv, page, D = _pages(w, k_cache, v_cache, weights)
+    B, max_pages = _batch(w, kv_len, page_table)
+    if dst_table.dim() != 2 or dst_table.shape[0] != B:
+        _bad(w, "dst_table must be [B, dst_max_pages]")
+    if keep_idx.dim() != 3 or tuple(keep_idx.shape[:2]) != (B, Hkv):
+        _bad(w, "keep_idx must be [B, H_kv, n_keep]")
+    if kv_len_out is not None and kv_len_out.shape != kv_len.shape:
+        _bad(w, "kv_len_out must be [B]")
+    i32 = torch.int32
+    _same_device(w, k_cache, (("k_cache", k_cache, k_cache.dtype), ("v_cache", v_cache, k_cache.dtype),
+                              ("weights", weights, torch.float32), ("page_table", page_table, i32),
+                              ("kv_len", kv_len, i32), ("dst_table", dst_table, i32), ("keep_idx", keep_idx, i32),
+                              ("kv_len_out", kv_len_out, i32)))
+    _launch(w, load_library().mea_paged_evict, k_cache.device, stream, _ptr(k_cache), _ptr(v_cache), _ptr(weights),
+            _ptr(page_table), _ptr(kv_len), _ptr(dst_table), _ptr(kv_len_out), _ptr(keep_idx), B, Hkv, D, pages, page,
+            max_pages, dst_table.shape[1], keep_idx.shape[2], int(n_recent), _dtype_code(k_cache))
+
+
+def paged_evict(k_cache, v_cache, weights, page_table, kv_len, dst_table, n_keep: int, n_recent: int, stream=None):
+    """Allocate (keep_idx, kv_len_out) with torch and run ``mea_paged_evict``."""
+    _pages("paged_evict", k_cache)
+    if n_keep < 1:
+        _bad("paged_evict", "n_keep below 1")
+    with _allocating(stream, k_cache.device):
+        idx = torch.empty((kv_len.shape[0], k_cache.shape[1], n_keep), dtype=torch.int32, device=k_cache.device)
+        out = torch.empty_like(kv_len)
+    mea_paged_evict(k_cache, v_cache, weights, page_table, kv_len, dst_table, out, idx, n_recent, stream)
+    return idx, out
 
 
 def mea_selftest_bounded_wait(gave_up, stream=None) -> None:

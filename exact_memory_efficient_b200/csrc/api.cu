@@ -10,6 +10,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "api_internal.h"
 #include "kernels.h"
 #include "mea_attn.h"
 #include "ptx.cuh"
@@ -273,6 +274,35 @@ mea_status_t common_checks(int B, int H, int Nq, int Nk, int D, float scale, mea
 
 }  // namespace
 
+namespace mea {
+
+mea_status_t api_fail(mea_status_t st, const char* where, const char* detail) { return fail(st, where, detail); }
+
+mea_status_t api_cuda(cudaError_t e, const char* where) { return cuda_status(e, where); }
+
+mea_status_t api_device(int* sm_count) {
+    DeviceInfo* d = nullptr;
+    const mea_status_t st = device_info(&d);
+    if (st == MEA_OK) *sm_count = d->sm_count;
+    return st;
+}
+
+mea_status_t api_map_bf16(CUtensorMap* m, const void* base, const cuuint64_t (&dims)[3],
+                          const cuuint64_t (&strides)[2], const cuuint32_t (&box)[3], const char* what) {
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+                                estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        char buf[96];
+        std::snprintf(buf, sizeof(buf), "CUresult %d (%s)", (int)r, what);
+        return fail(MEA_ERR_CUDA, "cuTensorMapEncodeTiled", buf);
+    }
+    return MEA_OK;
+}
+
+}  // namespace mea
+
 extern "C" {
 
 const char* mea_status_string(mea_status_t s) {
@@ -284,6 +314,7 @@ const char* mea_status_string(mea_status_t s) {
         case MEA_ERR_WORKSPACE: return "MEA_ERR_WORKSPACE: workspace missing or too small";
         case MEA_ERR_CUDA: return "MEA_ERR_CUDA: CUDA call or launch failed";
         case MEA_ERR_TIMEOUT: return "MEA_ERR_TIMEOUT: a device-side bounded wait expired";
+        case MEA_ERR_PAGE: return "MEA_ERR_PAGE: a page table entry, length or offset in device memory is out of range";
     }
     return "MEA_ERR_UNKNOWN";
 }
@@ -819,7 +850,8 @@ mea_status_t mea_last_device_error(void* stream) {
     if (flag == 0) return MEA_OK;
     const unsigned int zero = 0;
     if (cudaMemcpyToSymbol(mea::g_device_error, &zero, sizeof(zero)) != cudaSuccess) return MEA_ERR_CUDA;
-    return (flag & 1u) ? MEA_ERR_TIMEOUT : MEA_ERR_CUDA;
+    if (flag & mea::MEA_DEVERR_TIMEOUT) return MEA_ERR_TIMEOUT;
+    return (flag & mea::MEA_DEVERR_PAGE) ? MEA_ERR_PAGE : MEA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -150,4 +150,96 @@ cudaError_t launch_bwd_bf16(const Bf16BwdArgs& a, cudaStream_t stream, unsigned 
 // out[i] = mul * acc[i] as bf16 (round to nearest even) or fp32; n a multiple of 4.
 cudaError_t launch_accum_convert(const float* acc, void* out, long long n, float mul, bool bf16, cudaStream_t stream);
 
+// A ragged batch over a paged cache (paged.cuh).  cu_q [B + 1], kv_len [B] and
+// page_table [B, max_pages] are device memory; pages hold 1 << page_shift keys
+// of each of the Hkv heads: k, v [num_pages, Hkv, 1 << page_shift, D].
+struct PagedBatch {
+    const int* cu_q;
+    const int* kv_len;
+    const int* page_table;
+    int B, T, max_pages, page_shift, num_pages;
+};
+
+// Rotary positions (rope.cu).  Element strides of x and y per batch entry,
+// token and head; freq holds rot / 2 fp64 angles per position.
+struct RopeArgs {
+    const void* x;
+    void* y;
+    const int* positions;      // position of token n of batch entry b: positions[b * pos_batch + n]
+    const double* freq;
+    long long x_batch, x_head, x_token, y_batch, y_head, y_token, pos_batch;
+    int B, H, N, D, rot;
+    bool interleaved, inverse;
+    float mscale;
+};
+cudaError_t launch_rope(const RopeArgs& a, bool bf16, int sm_count, cudaStream_t stream);
+
+// The new tokens' q rotated, k rotated and v written to their pages, the slots'
+// weights cleared (rope.cu).  q, k, v: [T, heads, D] with token strides.
+struct AppendArgs {
+    PagedBatch s;
+    const void* q;
+    void* q_out;
+    const void* k;
+    const void* v;
+    void* k_cache;
+    void* v_cache;
+    float* weights;            // nullptr: the cache keeps none
+    const int* positions;      // nullptr: the position is the slot
+    const double* freq;        // nullptr: no rotation
+    long long q_stride, k_stride, v_stride;
+    int H, Hkv, D, rot;
+    bool interleaved;
+    float mscale;
+};
+cudaError_t launch_append(const AppendArgs& a, bool bf16, int sm_count, cudaStream_t stream);
+
+// Attention of the packed rows over the pages (paged_attn.cu).
+struct PagedAttnArgs {
+    PagedBatch s;
+    const void* q;
+    const void* k;
+    const void* v;
+    void* o;
+    float* lse;
+    float* part_acc;           // [nsplit, T, H, D] when nsplit > 1
+    float* part_ml;            // [nsplit, T, H, 2]
+    long long q_stride;
+    int H, Hkv, D;
+    int rows;                  // rows per tile: 1, 2, 4 or 8
+    int nsplit;                // chunks of every tile's keys
+    float scale;
+};
+int paged_simt_blocks_per_sm(bool bf16, int D, int rows);
+cudaError_t launch_paged_simt(const PagedAttnArgs& a, bool bf16, cudaStream_t stream);
+// Merge of the nsplit chunk summaries of every packed row of a sequence.
+cudaError_t launch_paged_merge(const PagedAttnArgs& a, bool bf16, cudaStream_t stream);
+
+// Accumulated attention weights (paged_weights.cu).
+struct PagedWeightsArgs {
+    PagedBatch s;
+    const void* q;
+    const float* lse;          // [T, H]
+    const void* k;
+    float* weights;            // [num_pages, Hkv, page]
+    long long q_stride;
+    int H, Hkv, D, max_kv;
+    float scale;
+};
+cudaError_t launch_paged_weights_simt(const PagedWeightsArgs& a, bool bf16, cudaStream_t stream);
+
+// Eviction (paged_evict.cu).
+struct EvictArgs {
+    PagedBatch s;              // cu_q unused
+    void* k;
+    void* v;
+    float* weights;
+    const int* dst_table;      // [B, dst_max_pages]
+    int* kv_len_out;
+    int* keep_idx;             // [B, Hkv, n_keep]
+    int Hkv, D, dst_max_pages, n_keep, n_recent;
+    bool in_place;             // dst_table is page_table
+};
+cudaError_t launch_evict(const EvictArgs& a, bool bf16, int sm_count, cudaStream_t stream);
+
 }  // namespace mea

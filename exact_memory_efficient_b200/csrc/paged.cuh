@@ -1,0 +1,81 @@
+// paged.cuh -- how the kernels of the paged key/value cache read a ragged
+// batch: packed rows, lengths and page tables, all in device memory.
+//
+// Nothing in device memory can be checked on the host, so each value is
+// brought into range before it is used as an index, and a value that was out
+// of range is recorded in the per-device error word (MEA_DEVERR_PAGE): a bad
+// table costs wrong results for its sequence, never an access outside the
+// caller's buffers.
+#pragma once
+
+#include <cstdint>
+
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace mea {
+
+// Sequence b of the batch: its rows [q0, q0 + n) of the packed tensors and its
+// L cached keys, the n new ones last.
+struct Seq {
+    int q0, n, L;
+};
+
+__device__ __forceinline__ Seq load_seq(const PagedBatch& s, int b) {
+    const int lo = s.cu_q ? s.cu_q[b] : 0;
+    const int hi = s.cu_q ? s.cu_q[b + 1] : 0;
+    const int len = s.kv_len[b];
+    const int cap = s.max_pages << s.page_shift;
+    Seq r;
+    r.q0 = min(max(lo, 0), s.T);
+    const int q1 = min(max(hi, r.q0), s.T);
+    r.n = q1 - r.q0;
+    r.L = min(max(len, 0), cap);
+    if (r.q0 != lo || q1 != hi || r.L != len) flag_bad_page();
+    return r;
+}
+
+// Page of the sequence's keys [i << page_shift, (i + 1) << page_shift), i < max_pages.
+__device__ __forceinline__ int load_page(const PagedBatch& s, int b, int i) {
+    const int p = s.page_table[(size_t)b * s.max_pages + i];
+    if ((unsigned)p < (unsigned)s.num_pages) return p;
+    flag_bad_page();
+    return 0;
+}
+
+// Packed rows are cut into tiles of `per` rows that start anew with every
+// sequence.  Tile x belongs to the sequence b with start(b) <= x < start(b + 1),
+// where start(b) = floor(cu_q[b] * mul / per) + b: since
+// ceil(n / per) <= floor((c + n) / per) - floor(c / per) + 1, the tiles of
+// different sequences never share an x, and a launch needs T * mul / per + B of
+// them, which the host knows without the lengths.  Returns b, or -1 when x is
+// in front of the first sequence; *tile is the tile's number in its sequence
+// (it may lie behind the sequence's end: the caller leaves then).
+__device__ __forceinline__ int find_tile(const PagedBatch& s, int x, int mul, int per, int* tile) {
+    int lo = 0, hi = s.B - 1;   // the last b whose start is at or below x
+    auto start = [&](int b) {
+        return (int)((long long)min(max(s.cu_q[b], 0), s.T) * mul / per) + b;
+    };
+    if (x < start(0)) return -1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (start(mid) <= x) lo = mid;
+        else hi = mid - 1;
+    }
+    *tile = x - start(lo);
+    return lo;
+}
+
+// The sequence of packed row t (-1: in front of the first or behind the last).
+__device__ __forceinline__ int find_row(const PagedBatch& s, int t) {
+    if (t < s.cu_q[0] || t >= s.cu_q[s.B]) return -1;
+    int lo = 0, hi = s.B - 1;   // the last b with cu_q[b] <= t
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (s.cu_q[mid] <= t) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+}  // namespace mea

@@ -15,6 +15,8 @@ namespace mea {
 // Per-device error word (defined in api.cu). Non-zero after a bounded wait expired.
 extern __device__ unsigned int g_device_error;
 constexpr unsigned int MEA_DEVERR_TIMEOUT = 1u;
+// A page table entry, length or offset read from device memory was out of range.
+constexpr unsigned int MEA_DEVERR_PAGE = 2u;
 
 // Wall-clock limit of one bounded wait, in nanoseconds (1 s).
 constexpr unsigned long long kWaitLimitNs = 1000000000ull;
@@ -31,6 +33,10 @@ __device__ __forceinline__ unsigned long long globaltimer_ns() {
 
 __device__ __forceinline__ void flag_timeout() {
     atomicOr(&g_device_error, MEA_DEVERR_TIMEOUT);
+}
+
+__device__ __forceinline__ void flag_bad_page() {
+    atomicOr(&g_device_error, MEA_DEVERR_PAGE);
 }
 
 __device__ __forceinline__ unsigned lane_id() { return threadIdx.x & 31u; }

@@ -1,0 +1,252 @@
+// rope.cu -- rotary positions: the rotation of q and k by their tokens'
+// positions, on its own (mea_rope, forward and gradient) and on the way into
+// the paged cache (mea_paged_append).
+//
+// Pair i of a head's first `rot` values is turned by the angle pos * freq_i
+// and scaled by mscale:
+//     (a, b) -> mscale (a cos - b sin, b cos + a sin);
+// the pairs are (x_2i, x_2i+1) (interleaved) or (x_i, x_i+rot/2).  The map is
+// linear, so its gradient is the transposed map: the same with -sin.
+//
+// An angle of 1e6 radians has a spacing of 0.06 in fp32, so angles are formed
+// in fp64 as revolutions, pos * freq / 2pi, brought into [-1/2, 1/2] by taking
+// off the nearest whole number (exact), and only then rounded to fp32 for
+// sincospif: the error left is 2^-24 of half a turn plus 2^-52 of the
+// revolutions.  Products are fp32, each result is rounded once.
+//
+// A thread owns one 16-byte vector of a head (two at the distance rot / 2 for
+// the half layout) of one token, forms its 2 to 8 sines and cosines once, and
+// walks over a slice of the heads with them.
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "kernels.h"
+#include "paged.cuh"
+#include "ptx.cuh"
+
+namespace mea {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr double kInvTwoPi = 0.15915494309189533577;
+
+template <typename T>
+constexpr int kVec = 16 / (int)sizeof(T);   // values per 16-byte vector
+
+template <typename T>
+__device__ __forceinline__ void unpack(const uint4& u, float (&x)[kVec<T>]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(w[i]);
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 pack(const float (&x)[kVec<T>]) {
+    if constexpr (sizeof(T) == 2)
+        return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                          pack_bf16x2(x[6], x[7]));
+    else
+        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                          __float_as_uint(x[3]));
+}
+
+__device__ __forceinline__ uint4 load16(const void* p) { return *static_cast<const uint4*>(p); }
+__device__ __forceinline__ void store16(void* p, const uint4& u) { *static_cast<uint4*>(p) = u; }
+
+// Units of one head: the vectors (or vector pairs) that a thread owns.
+template <typename T, bool INTER>
+__host__ __device__ __forceinline__ int turned_units(int rot) {
+    return INTER ? rot / kVec<T> : rot / (2 * kVec<T>);
+}
+template <typename T, bool INTER>
+__host__ __device__ __forceinline__ int head_units(int D, int rot) {
+    return turned_units<T, INTER>(rot) + (D - rot) / kVec<T>;
+}
+
+// Sines and cosines of a unit's pairs (VEC / 2 of them interleaved, VEC in the half layout).
+template <typename T, bool INTER>
+struct Turn {
+    static constexpr int kPairs = INTER ? kVec<T> / 2 : kVec<T>;
+    float c[kPairs], s[kPairs];
+    __device__ __forceinline__ void load(const double* freq, int unit, int pos, float mscale, bool inverse) {
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+            const double rev = (double)pos * (freq[unit * kPairs + i] * kInvTwoPi);
+            const float half_turns = 2.f * (float)(rev - rint(rev));
+            float sn, cs;
+            sincospif(half_turns, &sn, &cs);
+            c[i] = cs * mscale;
+            s[i] = (inverse ? -sn : sn) * mscale;
+        }
+    }
+};
+
+// Heads [0, heads) of one token: x and y point at the first head's first value.
+// `unit` < turned_units turns, the others copy one vector.
+template <typename T, bool INTER>
+__device__ __forceinline__ void turn_heads(const T* x, long long x_head, T* y, long long y_head, int heads, int unit,
+                                           int rot, const Turn<T, INTER>& t) {
+    constexpr int V = kVec<T>;
+    const int turned = turned_units<T, INTER>(rot);
+    if (unit >= turned) {
+        const int d = rot + (unit - turned) * V;
+#pragma unroll 4
+        for (int h = 0; h < heads; ++h) store16(y + h * y_head + d, load16(x + h * x_head + d));
+        return;
+    }
+    const int d = unit * V;
+#pragma unroll 4
+    for (int h = 0; h < heads; ++h) {
+        const T* xp = x + h * x_head + d;
+        T* yp = y + h * y_head + d;
+        float a[V], r[V];
+        if constexpr (INTER) {
+            unpack<T>(load16(xp), a);
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) {
+                r[2 * i] = a[2 * i] * t.c[i] - a[2 * i + 1] * t.s[i];
+                r[2 * i + 1] = a[2 * i + 1] * t.c[i] + a[2 * i] * t.s[i];
+            }
+            store16(yp, pack<T>(r));
+        } else {
+            float b[V], q[V];
+            unpack<T>(load16(xp), a);
+            unpack<T>(load16(xp + rot / 2), b);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                r[i] = a[i] * t.c[i] - b[i] * t.s[i];
+                q[i] = b[i] * t.c[i] + a[i] * t.s[i];
+            }
+            store16(yp, pack<T>(r));
+            store16(yp + rot / 2, pack<T>(q));
+        }
+    }
+}
+
+// grid.x: B * N * units threads, grid.y: slices of per_slice heads.
+template <typename T, bool INTER>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a, int units, int per_slice) {
+    const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
+    if (id >= (long long)a.B * a.N * units) return;
+    const long long row = id / units;
+    const int unit = (int)(id - row * units);
+    const long long b = row / a.N;
+    const long long n = row - b * a.N;
+    const int h0 = (int)blockIdx.y * per_slice;
+    Turn<T, INTER> t;
+    if (unit < turned_units<T, INTER>(a.rot))
+        t.load(a.freq, unit, a.positions[b * a.pos_batch + n], a.mscale, a.inverse);
+    const T* x = static_cast<const T*>(a.x) + b * a.x_batch + n * a.x_token + h0 * a.x_head;
+    T* y = static_cast<T*>(a.y) + b * a.y_batch + n * a.y_token + h0 * a.y_head;
+    turn_heads<T, INTER>(x, a.x_head, y, a.y_head, min(per_slice, a.H - h0), unit, a.rot, t);
+}
+
+// grid.x: T * units threads; grid.y: slices of q's heads, then of k's, then of v's.
+template <typename T, bool INTER>
+__global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a, int units, int copy_units, int per_slice,
+                                                          int q_slices, int kv_slices) {
+    const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
+    const bool is_v = (int)blockIdx.y >= q_slices + kv_slices;
+    const int u = is_v ? copy_units : units;
+    if (id >= (long long)a.s.T * u) return;
+    const int tok = (int)(id / u);
+    const int unit = (int)(id - (long long)tok * u);
+    const int b = find_row(a.s, tok);
+    if (b < 0) return;   // rows outside every sequence stay as they were
+    const bool is_q = (int)blockIdx.y < q_slices;
+    const bool turns = !is_v && unit < turned_units<T, INTER>(a.rot);
+    int slot = 0;
+    if (!is_q || (turns && a.positions == nullptr)) {
+        const Seq sq = load_seq(a.s, b);
+        if (tok < sq.q0 || tok >= sq.q0 + sq.n) return;   // offsets that run backwards
+        slot = sq.L - sq.n + (tok - sq.q0);
+    }
+    Turn<T, INTER> t;
+    if (turns) t.load(a.freq, unit, a.positions ? a.positions[tok] : slot, a.mscale, false);
+    if (is_q) {
+        const int h0 = (int)blockIdx.y * per_slice;
+        turn_heads<T, INTER>(static_cast<const T*>(a.q) + tok * a.q_stride + (long long)h0 * a.D, a.D,
+                             static_cast<T*>(a.q_out) + ((long long)tok * a.H + h0) * a.D, a.D,
+                             min(per_slice, a.H - h0), unit, a.rot, t);
+        return;
+    }
+    if (slot < 0) return;   // more new tokens than keys: the first ones have no slot
+    const long long head = 1LL << a.s.page_shift;   // keys of one head in a page
+    const long long first = (long long)load_page(a.s, b, slot >> a.s.page_shift) * a.Hkv;
+    const int h0 = ((int)blockIdx.y - q_slices - (is_v ? kv_slices : 0)) * per_slice;
+    const int heads = min(per_slice, a.Hkv - h0);
+    const long long key = (first + h0) * head + (slot & ((1 << a.s.page_shift) - 1));
+    if (is_v) {
+        const T* x = static_cast<const T*>(a.v) + tok * a.v_stride + (long long)h0 * a.D + unit * kVec<T>;
+        T* y = static_cast<T*>(a.v_cache) + key * a.D + unit * kVec<T>;
+#pragma unroll 4
+        for (int h = 0; h < heads; ++h) store16(y + h * head * a.D, load16(x + (long long)h * a.D));
+        if (a.weights != nullptr && unit == 0)
+            for (int h = 0; h < heads; ++h) a.weights[key + h * head] = 0.f;
+        return;
+    }
+    turn_heads<T, INTER>(static_cast<const T*>(a.k) + tok * a.k_stride + (long long)h0 * a.D, a.D,
+                         static_cast<T*>(a.k_cache) + key * a.D, head * a.D, heads, unit, a.rot, t);
+}
+
+// Heads per thread: as many as leave every SM some 1,024 threads (the sines are
+// formed once per slice), at most 8.
+int heads_per_slice(long long threads_per_head, int H, int sm_count) {
+    const long long per = threads_per_head * H / ((long long)sm_count * 1024);
+    return per < 1 ? 1 : per > 8 ? 8 : (int)per;
+}
+
+template <typename T, bool INTER>
+cudaError_t launch_rope_t(const RopeArgs& a, int sm_count, cudaStream_t stream) {
+    const int units = head_units<T, INTER>(a.D, a.rot);
+    const long long threads = (long long)a.B * a.N * units;
+    const int per = heads_per_slice(threads, a.H, sm_count);
+    const long long blocks = (threads + kThreads - 1) / kThreads;
+    const int slices = (a.H + per - 1) / per;
+    if (blocks > 0x7fffffffLL || slices > 65535) return cudaErrorInvalidValue;
+    rope_kernel<T, INTER><<<dim3((unsigned)blocks, (unsigned)slices), kThreads, 0, stream>>>(a, units, per);
+    return cudaGetLastError();
+}
+
+template <typename T, bool INTER>
+cudaError_t launch_append_t(const AppendArgs& a, int sm_count, cudaStream_t stream) {
+    const int units = head_units<T, INTER>(a.D, a.rot);
+    const int copy_units = a.D / kVec<T>;
+    const int heads = a.H + 2 * a.Hkv;
+    const int per = heads_per_slice((long long)a.s.T * units, heads, sm_count);
+    const int q_slices = (a.H + per - 1) / per;
+    const int kv_slices = (a.Hkv + per - 1) / per;
+    const long long blocks = ((long long)a.s.T * copy_units + kThreads - 1) / kThreads;   // copy_units >= units
+    if (blocks > 0x7fffffffLL || q_slices + 2 * kv_slices > 65535) return cudaErrorInvalidValue;
+    append_kernel<T, INTER><<<dim3((unsigned)blocks, (unsigned)(q_slices + 2 * kv_slices)), kThreads, 0, stream>>>(
+        a, units, copy_units, per, q_slices, kv_slices);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const RopeArgs& a, bool bf16, int sm_count, cudaStream_t stream) {
+    if (bf16)
+        return a.interleaved ? launch_rope_t<uint16_t, true>(a, sm_count, stream)
+                             : launch_rope_t<uint16_t, false>(a, sm_count, stream);
+    return a.interleaved ? launch_rope_t<float, true>(a, sm_count, stream)
+                         : launch_rope_t<float, false>(a, sm_count, stream);
+}
+
+cudaError_t launch_append(const AppendArgs& a, bool bf16, int sm_count, cudaStream_t stream) {
+    if (bf16)
+        return a.interleaved ? launch_append_t<uint16_t, true>(a, sm_count, stream)
+                             : launch_append_t<uint16_t, false>(a, sm_count, stream);
+    return a.interleaved ? launch_append_t<float, true>(a, sm_count, stream)
+                         : launch_append_t<float, false>(a, sm_count, stream);
+}
+
+}  // namespace mea

@@ -68,7 +68,8 @@ typedef enum {
     MEA_ERR_MISALIGNED = 3,   /* a pointer violates the alignment rule above */
     MEA_ERR_WORKSPACE = 4,    /* workspace missing or smaller than mea_attn_bwd_workspace_size */
     MEA_ERR_CUDA = 5,         /* a CUDA runtime/driver call or a launch failed */
-    MEA_ERR_TIMEOUT = 6       /* a device-side bounded wait expired (see mea_last_device_error) */
+    MEA_ERR_TIMEOUT = 6,      /* a device-side bounded wait expired (see mea_last_device_error) */
+    MEA_ERR_PAGE = 7          /* device memory held a page, length or offset out of range (ditto) */
 } mea_status_t;
 
 typedef enum {
@@ -386,10 +387,168 @@ mea_status_t mea_attn_bwd_noalloc(const void* q, const void* k, const void* v,
                                   int B, int H, int Nq, int Nk, int D, float scale,
                                   mea_dtype_t dtype, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Rotary positions and the paged key/value cache
+ *
+ * A serving step over a cache in pages is: mea_paged_append (rotate the new
+ * tokens' q and k, write k and v to their pages), mea_attn_paged (attention of
+ * the new tokens), and, where the cache is bounded, mea_attn_paged_weights
+ * (add up the attention that every cached key received) and mea_paged_evict
+ * (keep the heaviest and the most recent keys).  mea_rope is the rotation on
+ * its own, forward and gradient, for training.
+ *
+ * Layout of a batch of B sequences with new tokens:
+ *  - New tokens are packed sequence after sequence: q [T, H, D], k and v
+ *    [T, H_kv, D], each with a token stride in elements (slices of one
+ *    projection need no copy); heads and head dims are dense.  Strides are
+ *    multiples of 8 and at least heads * D.  o [T, H, D] and lse [T, H] (fp32)
+ *    are dense.  Sequence b owns the rows cu_q[b] <= t < cu_q[b + 1]; cu_q
+ *    [B + 1] int32 is not decreasing and at most T.  Rows outside every
+ *    sequence are neither read nor written.
+ *  - The cache is num_pages pages of page_size keys (16, 32, 64, 128 or 256):
+ *    k_cache, v_cache [num_pages, H_kv, page_size, D], and, where it is
+ *    bounded, weights [num_pages, H_kv, page_size] fp32.
+ *  - kv_len [B] int32 counts the cached keys of each sequence, its n new ones
+ *    included; key j of sequence b is slot j % page_size of page
+ *    page_table[b][j / page_size], with page_table [B, max_pages] int32.
+ *    Entries behind a sequence's last key are not read.
+ *  - New token i of n sees the keys j < kv_len - n + i + 1: all cached ones,
+ *    and the new ones up to itself.  Query head h reads key/value head
+ *    h / (H / H_kv).  A row that sees no key (kv_len < n) has o = 0 and
+ *    lse = -inf.
+ *  - Slots behind a sequence's last key may hold anything, NaN included.  Keys
+ *    and values of a sequence that hold inf or NaN make that sequence's rows
+ *    undefined, and no others.
+ *  - max_q and max_kv are the caller's bounds on the new tokens and the cached
+ *    keys of one sequence.  They only choose the launch: results are right
+ *    whatever they are, and a captured graph may be replayed with other
+ *    lengths, offsets and tables in the same buffers.
+ *  - cu_q, kv_len and page_table are device memory and cannot be checked when
+ *    the call is made.  A value out of range makes the results of its sequence
+ *    (with offsets that run backwards: of the call) undefined, but no access
+ *    leaves the buffers given here; mea_last_device_error() then reports
+ *    MEA_ERR_PAGE.
+ *  - dtype, head dims, ownership, streams and errors as above: bf16 with D 64
+ *    or 128, fp32 with D 32, 64, 96 or 128.  T == 0 or B == 0 is a no-op.
+ *  - B and H_kv are at most 65535.
+ */
+typedef enum {
+    MEA_ROPE_HALF = 0,        /* pairs (i, i + rot_dim / 2) */
+    MEA_ROPE_INTERLEAVED = 1  /* pairs (2 i, 2 i + 1) */
+} mea_rope_layout_t;
+
+typedef enum {
+    MEA_ROPE_SCALE_NONE = 0,
+    MEA_ROPE_SCALE_LINEAR = 1,  /* every angle divided by factor */
+    MEA_ROPE_SCALE_BASE = 2,    /* base * factor^(r / (r - 2)): the slowest pair slows down by factor */
+    MEA_ROPE_SCALE_BY_PARTS = 3 /* pairs that turn less than `slow` times over original_len slow down by
+                                   factor, those above `fast` times keep their speed, a linear mix between */
+} mea_rope_scaling_t;
+
+/*
+ * Host function: the rot_dim / 2 angles per position, in radians, as the other
+ * entry points take them (in device memory): base^(-2 i / rot_dim), scaled for
+ * contexts longer than the model's.  `freq` is HOST memory.  original_len,
+ * slow and fast count for BY_PARTS only.  rot_dim even; base > 1; factor >= 1.
+ * Errors: MEA_ERR_INVALID_ARG.
+ */
+mea_status_t mea_rope_frequencies(double* freq, int rot_dim, double base, mea_rope_scaling_t scaling, double factor,
+                                  double original_len, double slow, double fast);
+
+/*
+ * y = mscale * R(position) x: each pair (a, b) of the first rot_dim values of
+ * every head turns by position * freq[i], (a cos - b sin, b cos + a sin); the
+ * values behind rot_dim are copied unscaled.  inverse != 0 turns the other way:
+ * the gradient of the map (dx from dy, with the same mscale).
+ *
+ * x, y [B, H, N, D]; y may be x.  positions int32 [N], or [B, N] with
+ * positions_per_batch != 0; any value.  freq fp64 [rot_dim / 2] in device
+ * memory.  rot_dim a multiple of 16, at most D.  Angles are formed in fp64,
+ * products in fp32, each result is rounded once.  Errors:
+ * MEA_ERR_INVALID_ARG, MEA_ERR_UNSUPPORTED, MEA_ERR_MISALIGNED, MEA_ERR_CUDA.
+ */
+mea_status_t mea_rope(const void* x, void* y, const int* positions, const double* freq, int B, int H, int N, int D,
+                      int rot_dim, int positions_per_batch, mea_rope_layout_t layout, float mscale, int inverse,
+                      mea_dtype_t dtype, void* stream);
+
+/*
+ * Writes the new tokens into the cache: k turned as by mea_rope and v, into
+ * the slots kv_len - n .. kv_len - 1 of their sequence, the slots' weights set
+ * to 0 (weights may be NULL).  q_out [T, H, D] receives q turned the same way
+ * (q and q_out NULL: no queries).  positions int32 [T] (NULL: a token's slot is
+ * its position); freq NULL: no rotation, rot_dim, layout and mscale are not
+ * read.  q_out may be q where q is dense.  With kv_len < n the first new tokens
+ * have no slot and are not stored.  Two sequences of a call must not write the
+ * same page.  Errors: MEA_ERR_INVALID_ARG, MEA_ERR_UNSUPPORTED,
+ * MEA_ERR_MISALIGNED, MEA_ERR_CUDA.
+ */
+mea_status_t mea_paged_append(const void* q, void* q_out, const void* k, const void* v, void* k_cache, void* v_cache,
+                              float* weights, const int* cu_q, const int* kv_len, const int* page_table,
+                              const int* positions, const double* freq, int T, int B, int H, int H_kv, int D,
+                              long long q_stride, long long k_stride, long long v_stride, int num_pages,
+                              int page_size, int max_pages, int rot_dim, mea_rope_layout_t layout, float mscale,
+                              mea_dtype_t dtype, void* stream);
+
+/*
+ * o_i = sum_j softmax_j(scale * q_i . k_j) v_j and lse_i over the keys that new
+ * token i sees.  One new token per sequence is the decode form.  workspace:
+ * device memory of at least mea_attn_paged_workspace_size bytes for the same
+ * sizes and bounds on the current device (it depends on the SM count), 16-byte
+ * aligned, scratch; two calls that may overlap on the GPU need one each.  The
+ * same inputs give the same bits.  Errors: MEA_ERR_INVALID_ARG,
+ * MEA_ERR_UNSUPPORTED, MEA_ERR_MISALIGNED, MEA_ERR_WORKSPACE, MEA_ERR_CUDA.
+ */
+mea_status_t mea_attn_paged_workspace_size(int T, int B, int H, int H_kv, int D, int max_q, int max_kv,
+                                           mea_dtype_t dtype, size_t* bytes);
+
+mea_status_t mea_attn_paged(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse,
+                            const int* cu_q, const int* kv_len, const int* page_table, int T, int B, int H, int H_kv,
+                            int D, long long q_stride, int num_pages, int page_size, int max_pages, int max_q,
+                            int max_kv, float scale, mea_dtype_t dtype, void* workspace, size_t workspace_bytes,
+                            void* stream);
+
+/*
+ * weights_j += sum over the rows i of the call's query heads of the key's group
+ * that see key j of exp(scale * q_i . k_j - lse_i), with lse [T, H] from
+ * mea_attn_paged of the same call: what key j contributed.  Every sum has one
+ * owner and a fixed order (no atomics): the same inputs give the same bits.
+ * Two sequences of a call must not share a page here (each would add to the
+ * same sums).  Errors: MEA_ERR_INVALID_ARG, MEA_ERR_UNSUPPORTED,
+ * MEA_ERR_MISALIGNED, MEA_ERR_CUDA.
+ */
+mea_status_t mea_attn_paged_weights(const void* q, const float* lse, const void* k_cache, float* weights,
+                                    const int* cu_q, const int* kv_len, const int* page_table, int T, int B, int H,
+                                    int H_kv, int D, long long q_stride, int num_pages, int page_size, int max_pages,
+                                    int max_q, int max_kv, float scale, mea_dtype_t dtype, void* stream);
+
+/*
+ * Cuts every sequence with more than n_keep cached keys to n_keep: each
+ * key/value head keeps its n_recent last keys and, of the others, the
+ * n_keep - n_recent with the largest weights (equal weights: the lower slot
+ * first; NaN counts as -inf).  The kept keys, values and weights go, in the
+ * order of their slots, to slots 0, 1, ... of the sequence's destination pages
+ * dst_table [B, dst_max_pages]; shorter sequences move whole.  Nothing else of
+ * the cache is written.  keep_idx [B, H_kv, n_keep] int32 receives the kept
+ * slots, -1 behind them; kv_len_out [B] (NULL, or kv_len itself) the new
+ * lengths min(kv_len, n_keep).
+ *
+ * dst_table == page_table (the same pointer, dst_max_pages == max_pages): in
+ * place.  Otherwise the destination pages must be none that the call reads.
+ * No two sequences may share a destination page.  Keys keep the rotation of
+ * their original positions.  0 <= n_recent <= n_keep, 1 <= n_keep;
+ * B * H_kv <= 65535.  Errors: MEA_ERR_INVALID_ARG, MEA_ERR_UNSUPPORTED,
+ * MEA_ERR_MISALIGNED, MEA_ERR_CUDA.
+ */
+mea_status_t mea_paged_evict(void* k_cache, void* v_cache, float* weights, const int* page_table, const int* kv_len,
+                             const int* dst_table, int* kv_len_out, int* keep_idx, int B, int H_kv, int D,
+                             int num_pages, int page_size, int max_pages, int dst_max_pages, int n_keep, int n_recent,
+                             mea_dtype_t dtype, void* stream);
+
 /*
  * Synchronises `stream`, then reads and clears the current device's error
  * flag.  Returns MEA_ERR_TIMEOUT if any kernel of this library gave up on a
- * bounded wait since the last call, MEA_ERR_CUDA if the synchronisation
+ * bounded wait since the last call, MEA_ERR_PAGE if a kernel of the paged cache
+ * met an entry out of range (see there), MEA_ERR_CUDA if the synchronisation
  * itself failed, MEA_OK otherwise.
  */
 mea_status_t mea_last_device_error(void* stream);

@@ -27,3 +27,5 @@ from .attention import (  # noqa: F401
     combine_partials,
     combine_two_blocks,
 )
+
+from . import paged  # noqa: F401,E402
