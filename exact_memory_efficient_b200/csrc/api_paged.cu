@@ -84,6 +84,7 @@ int simt_rows(int G, int max_q) {
 }
 
 struct AttnPlan {
+    int tt = 0;                // tokens per query tile of the tensor-core kernel; 0: the CUDA-core kernel
     int rows = 1;
     int nsplit = 1;
     size_t ws_bytes = 0;
@@ -92,6 +93,11 @@ struct AttnPlan {
 // Chunks of the keys so that the launch fills the device's slots about once.
 AttnPlan attn_plan(int sm_count, int T, int B, int H, int H_kv, int D, int max_q, int max_kv, bool bf16) {
     AttnPlan p;
+    if (bf16 && (p.tt = mea::paged_tc_tokens(H / H_kv, max_q)) > 0) {
+        p.rows = 2 * p.tt * (H / H_kv);
+        p.ws_bytes = (size_t)2 * sm_count * (p.rows * (D + 2) * sizeof(float) + sizeof(mea::PagedPart));
+        return p;
+    }
     p.rows = simt_rows(H / H_kv, max_q);
     const long long tiles = std::max(1LL, (long long)T * (H / H_kv) / p.rows) * H_kv;
     const long long slots = (long long)sm_count * mea::paged_simt_blocks_per_sm(bf16, D, p.rows);
@@ -268,6 +274,32 @@ mea_status_t mea_attn_paged(const void* q, const void* k_cache, const void* v_ca
             return api_fail(MEA_ERR_WORKSPACE, where, "workspace missing or below mea_attn_paged_workspace_size");
         if (!aligned(workspace, 16)) return MEA_ERR_MISALIGNED;
     }
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (p.tt > 0) {
+        mea::PagedTcArgs t;
+        const int G = H / H_kv;
+        const cuuint64_t q_dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)T};
+        const cuuint64_t q_strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)q_stride * 2};
+        const cuuint32_t q_box[3] = {64, (cuuint32_t)G, (cuuint32_t)p.tt};
+        const cuuint64_t k_dims[3] = {(cuuint64_t)D, (cuuint64_t)page_size, (cuuint64_t)num_pages * H_kv};
+        const cuuint64_t k_strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)page_size * D * 2};
+        const cuuint32_t k_box[3] = {64, (cuuint32_t)std::min(page_size, 128), 1};
+        if ((st = mea::api_map_bf16(&t.tm_q, q, q_dims, q_strides, q_box, "q")) != MEA_OK) return st;
+        if ((st = mea::api_map_bf16(&t.tm_k, k_cache, k_dims, k_strides, k_box, "k_cache")) != MEA_OK) return st;
+        if ((st = mea::api_map_bf16(&t.tm_v, v_cache, k_dims, k_strides, k_box, "v_cache")) != MEA_OK) return st;
+        t.s = batch_of(cu_q, kv_len, page_table, T, B, num_pages, page_size, max_pages);
+        t.o = o;
+        t.lse = lse;
+        t.part_acc = static_cast<float*>(workspace);
+        t.part_ml = t.part_acc + (size_t)2 * sms * p.rows * D;
+        t.parts = reinterpret_cast<mea::PagedPart*>(t.part_ml + (size_t)2 * sms * p.rows * 2);
+        t.H = H;
+        t.Hkv = H_kv;
+        t.D = D;
+        t.tt = p.tt;
+        t.scale = scale;
+        return mea::api_cuda(mea::launch_paged_tc(t, sms, s), where);
+    }
     mea::PagedAttnArgs a;
     a.s = batch_of(cu_q, kv_len, page_table, T, B, num_pages, page_size, max_pages);
     a.q = q;
@@ -284,7 +316,6 @@ mea_status_t mea_attn_paged(const void* q, const void* k_cache, const void* v_ca
     a.rows = p.rows;
     a.nsplit = p.nsplit;
     a.scale = scale;
-    const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if ((st = mea::api_cuda(mea::launch_paged_simt(a, bf16, s), where)) != MEA_OK || p.nsplit == 1) return st;
     return mea::api_cuda(mea::launch_paged_merge(a, bf16, s), where);
 }

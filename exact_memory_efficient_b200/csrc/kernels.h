@@ -215,6 +215,29 @@ cudaError_t launch_paged_simt(const PagedAttnArgs& a, bool bf16, cudaStream_t st
 // Merge of the nsplit chunk summaries of every packed row of a sequence.
 cudaError_t launch_paged_merge(const PagedAttnArgs& a, bool bf16, cudaStream_t stream);
 
+// The same on the tensor cores (paged_tc.cu), bf16.  Maps, 128-byte swizzle: q
+// {D, H, T} with box {64, G, tt}; k, v {D, page, num_pages * Hkv} with box
+// {64, min(page, 128), 1}.  Workspace of sm_count CTAs, two parts each of up to
+// 2 * tt * G rows: part_acc [2 sm_count, rows, D], part_ml [.., 2], parts [2 sm_count].
+struct PagedPart {
+    int b, h, i, t0, t1, n_kv;   // key tiles [t0, t1) of item i of (b, h); n_kv = 0: none
+};
+struct PagedTcArgs {
+    CUtensorMap tm_q, tm_k, tm_v;
+    PagedBatch s;
+    void* o;
+    float* lse;
+    float* part_acc;
+    float* part_ml;
+    PagedPart* parts;
+    int H, Hkv, D;
+    int tt;                    // tokens per query tile
+    float scale;
+};
+// Tokens per query tile for groups of G heads; 0: the kernel does not apply.
+int paged_tc_tokens(int G, int max_q);
+cudaError_t launch_paged_tc(const PagedTcArgs& a, int sm_count, cudaStream_t stream);
+
 // Accumulated attention weights (paged_weights.cu).
 struct PagedWeightsArgs {
     PagedBatch s;

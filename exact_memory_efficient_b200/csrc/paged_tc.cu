@@ -1,0 +1,809 @@
+// paged_tc.cu -- bf16 attention of ragged chunks of new tokens over a paged
+// cache on the 5th-generation tensor cores (sm_100a).
+//
+// Same definition as paged_attn.cu; per key block j the recurrence of
+// fwd_bf16.cu: m' = max(m, rowmax S_j), l' = l e^(m-m') + sum e^(S_j-m'),
+// O' = O e^(m-m') + e^(S_j-m') V_j, normalised once at the end.
+//
+// Work.  The rows of a key/value head are its (token, head of the group) pairs,
+// token by token; tt tokens (tt * G <= 128 rows) make a query tile and two
+// tiles an item, which needs the key tiles (128 keys) up to what its last
+// token sees.  Lengths are ragged and only known on the device, so the launch
+// has one CTA per SM, and each CTA takes an equal share of all key tiles of all
+// items (sequence by sequence, head by head, item by item): it begins and ends
+// inside an item where the share does.  A whole item goes straight to o and
+// lse; a part of one leaves its rows' summary (reference maximum, exp-sum,
+// unnormalised accumulator) in the CTA's first or second workspace slot, and
+// paged_tc_merge_kernel joins the parts of every item in the order of their
+// keys.  Every CTA finds its share by summing the key tiles of all sequences
+// itself; nothing is planned on the host, and a captured launch follows the
+// lengths that it finds.
+//
+// Roles and TMEM are those of fwd_persist.cu (320 threads):
+//   warp 0       TMEM allocator, then TMA producer: Q tiles per item, then K_0,
+//                V_0, K_1, V_1, ... of the item through the ring, one lane per
+//                (page, 64 head dims) box; no multicast.  Pages behind the
+//                sequence's last key are not looked up: their boxes lie outside
+//                the tensor and read as zero.
+//   warp 1       MMA issuer (one thread)
+//   warps 2-5    softmax / epilogue of slot 0, warps 6-9 of slot 1
+// Slot t holds query tile t of an item and the key tiles that tile sees; when
+// the item has one query tile both slots run it over alternate key tiles and
+// fold their summaries at the end.
+// S is masked per row (keys past the row's token).  The values behind a
+// sequence's last key in its last page may be anything, and 0 x NaN is NaN, so
+// the first slot that uses such a V tile overwrites those rows with zeros.
+// TMEM: S_0 [0,128) S_1 [128,256) O_0 [256,256+D) O_1 [384,384+D).
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "kernels.h"
+#include "paged.cuh"
+#include "ptx.cuh"
+#include "rows.cuh"
+
+namespace mea {
+namespace {
+
+constexpr int kTile = 128;        // query rows per tile, keys per tile
+constexpr int kThreads = 320;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kRescaleThreshold = 8.0f;
+constexpr float kNoKey = -1e30f;  // reference maximum of a row that has seen no key (finite: no inf - inf)
+constexpr unsigned kIdescNegateA = 1u << 13;
+
+template <int D>
+struct Cfg {
+    static constexpr int kQBytes = kTile * D * 2;
+    static constexpr int kTileBytes = kTile * D * 2;     // K or V tile
+    static constexpr int kStages = D == 128 ? 4 : 6;
+    static constexpr int kBoxBytes = 128 * 128;
+    static constexpr int kSmemData = 2 * kQBytes + kStages * kTileBytes;
+    static constexpr int kMergeBytes = 2 * kTile * 2 * 4;   // both slots' (m, l) per row
+    static constexpr int kSmemBytes = kSmemData + kMergeBytes + 1024 /*barriers*/ + 1024 /*alignment slack*/;
+    static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+};
+
+struct Barriers {
+    uint64_t q_full, q_empty;
+    uint64_t full[8], empty[8];
+    uint64_t s_full[2], p_half[2], p_ready[2], o_free[2];
+    uint64_t o_final, merge_ready, drain;
+    unsigned tmem_base;
+    int abort_flag;
+    // this CTA's share: where it begins, and its key tiles
+    int b0, h0, i0, t0;
+    long long tiles;
+    long long warp_sum[kThreads / 32];
+};
+
+// Items of a sequence, and the key tiles of item i (an item whose rows see no
+// key has one tile, fully masked, so that its rows are written).
+__device__ __forceinline__ int items_of(const Seq& sq, int tt) { return (sq.n + 2 * tt - 1) / (2 * tt); }
+__device__ __forceinline__ int keys_seen(const Seq& sq, int tokens) {   // by the last of the first `tokens`
+    return max(0, sq.L - sq.n + min(tokens, sq.n));
+}
+__device__ __forceinline__ int tiles_of(const Seq& sq, int tt, int i) {
+    return max(1, (keys_seen(sq, (i + 1) * 2 * tt) + kTile - 1) / kTile);
+}
+
+// Position in the list of items; walks on item by item.
+struct Walk {
+    Seq sq;
+    int b, h, i, items;
+    int t0, t1, n_kv;       // key tiles [t0, t1) of the item's n_kv
+    long long left;         // tiles of the share from t0 on
+    bool first;
+
+    __device__ __forceinline__ void begin(const PagedBatch& s, const Barriers* bars, int tt) {
+        b = bars->b0;
+        h = bars->h0;
+        i = bars->i0;
+        t0 = bars->t0;
+        left = bars->tiles;
+        first = true;
+        if (left > 0) {
+            sq = load_seq(s, b);
+            items = items_of(sq, tt);
+            n_kv = tiles_of(sq, tt, i);
+            t1 = (int)min((long long)n_kv, t0 + left);
+        }
+    }
+    __device__ __forceinline__ bool done() const { return left <= 0; }
+    __device__ __forceinline__ void next(const PagedBatch& s, int Hkv, int tt) {
+        left -= t1 - t0;
+        first = false;
+        if (left <= 0) return;
+        if (++i == items) {
+            i = 0;
+            if (++h == Hkv) {
+                h = 0;
+                do {   // sequences without new tokens have no item
+                    ++b;
+                    if (b >= s.B) {
+                        left = 0;
+                        return;
+                    }
+                    sq = load_seq(s, b);
+                } while (sq.n == 0);
+                items = items_of(sq, tt);
+            }
+        }
+        n_kv = tiles_of(sq, tt, i);
+        t0 = 0;
+        t1 = (int)min((long long)n_kv, left);
+    }
+    __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == n_kv; }
+    __device__ __forceinline__ bool two(int tt) const { return i * 2 * tt + tt < sq.n; }   // both query tiles live
+    // key tiles of [t0, t1) that query tile 0 of a two-tile item sees
+    __device__ __forceinline__ int tiles_slot0(int tt) const {
+        const int seen = (keys_seen(sq, i * 2 * tt + tt) + kTile - 1) / kTile;
+        return max(0, min(t1, seen) - t0);
+    }
+};
+
+// Every thread of the CTA: the share [W c / C, W (c + 1) / C) of all key tiles.
+__device__ __forceinline__ void find_share(const PagedTcArgs& a, Barriers* bars) {
+    const int tid = (int)threadIdx.x;
+    const unsigned lane = lane_id(), warp = warp_id();
+    auto of_seq = [&](int b) {
+        const Seq sq = load_seq(a.s, b);
+        const int items = items_of(sq, a.tt);
+        long long sum = 0;
+        for (int i = 0; i < items; ++i) sum += tiles_of(sq, a.tt, i);
+        return sum * a.Hkv;
+    };
+    // inclusive scan over the block's threads; returns the sum in front of this thread, *all the block's
+    auto scan = [&](long long x, long long* all) {
+        long long upto = x;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= (unsigned)o) upto += y;
+        }
+        if (lane == 31) bars->warp_sum[warp] = upto;
+        __syncthreads();
+        long long before = 0, total = 0;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < (int)warp) before += bars->warp_sum[w];
+            total += bars->warp_sum[w];
+        }
+        __syncthreads();
+        *all = total;
+        return before + upto - x;
+    };
+    long long W = 0, mine = 0, block_before = 0;
+    for (int b0 = 0; b0 < a.s.B; b0 += kThreads) {
+        const int b = b0 + tid;
+        long long all;
+        mine = b < a.s.B ? of_seq(b) : 0;
+        block_before = scan(mine, &all);
+        W += all;
+    }
+    const long long c = blockIdx.x, C = gridDim.x;
+    const long long w0 = W * c / C, w1 = W * (c + 1) / C;
+    if (tid == 0) bars->tiles = w1 - w0;
+    auto locate = [&](int b, long long before, long long sum) {
+        if (w0 < before || w0 >= before + sum || w1 <= w0) return;
+        const Seq sq = load_seq(a.s, b);
+        const int items = items_of(sq, a.tt);
+        const long long per_head = sum / a.Hkv;
+        long long x = w0 - before;
+        bars->b0 = b;
+        bars->h0 = (int)(x / per_head);
+        x -= bars->h0 * per_head;
+        int i = 0;
+        for (; i + 1 < items; ++i) {
+            const int n = tiles_of(sq, a.tt, i);
+            if (x < n) break;
+            x -= n;
+        }
+        bars->i0 = i;
+        bars->t0 = (int)x;
+    };
+    if (a.s.B <= kThreads) {
+        if (tid < a.s.B) locate(tid, block_before, mine);
+    } else {
+        long long base = 0;
+        for (int b0 = 0; b0 < a.s.B; b0 += kThreads) {
+            const int b = b0 + tid;
+            long long all;
+            const long long x = b < a.s.B ? of_seq(b) : 0;
+            const long long before = base + scan(x, &all);
+            if (b < a.s.B) locate(b, before, x);
+            base += all;
+        }
+    }
+    __syncthreads();
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                const __grid_constant__ CUtensorMap tm_v, const PagedTcArgs a) {
+    using C = Cfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint8_t* sQ = smem;
+    uint8_t* sRing = smem + 2 * C::kQBytes;
+    float* sMerge = reinterpret_cast<float*>(smem + C::kSmemData);
+    Barriers* bars = reinterpret_cast<Barriers*>(smem + C::kSmemData + C::kMergeBytes);
+
+    const unsigned warp = warp_id();
+    const unsigned lane = lane_id();
+    const int tt = a.tt;
+    const int G = a.H / a.Hkv;
+
+    if (threadIdx.x == 0) {
+        mbar_init(&bars->q_full, 1);
+        mbar_init(&bars->q_empty, 1);
+        for (int s = 0; s < C::kStages; ++s) {
+            mbar_init(&bars->full[s], 1);
+            mbar_init(&bars->empty[s], 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&bars->s_full[t], 1);
+            mbar_init(&bars->p_half[t], 128);
+            mbar_init(&bars->p_ready[t], 128);
+            mbar_init(&bars->o_free[t], 128);
+        }
+        mbar_init(&bars->o_final, 1);
+        mbar_init(&bars->merge_ready, 256);
+        mbar_init(&bars->drain, 1);
+        bars->abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(&bars->tmem_base, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const unsigned tmem = bars->tmem_base;
+    volatile int* abort_flag = &bars->abort_flag;
+    // programmatic stream serialisation: nothing global is touched before the
+    // previous kernel's results are complete and visible
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    find_share(a, bars);
+
+    Walk w;
+    w.begin(a.s, bars, tt);
+    if (warp == 0) {
+        // ------------------------------------------------ TMA producer
+        if (lane == 0) {
+            prefetch_tmap(&tm_q);
+            prefetch_tmap(&tm_k);
+            prefetch_tmap(&tm_v);
+            a.parts[2 * blockIdx.x].n_kv = 0;       // no part yet
+            a.parts[2 * blockIdx.x + 1].n_kv = 0;
+        }
+        const int shift = a.s.page_shift;
+        const int box_rows = min(kTile, 1 << shift);
+        constexpr int kHalves = D / 64;
+        const int boxes = kTile / box_rows * kHalves;    // of a tile: at most 16
+        const int my_row = (int)lane / kHalves * box_rows;   // lane's box: first key in the tile,
+        const int my_half = (int)lane % kHalves;              // 64 head dims
+        const bool mine = (int)lane < boxes;
+        const int outside = a.s.num_pages * a.Hkv;       // a page behind the tensor: reads as zero
+        int c_glob = 0;
+        int li = 0, q_asked = 0;    // items; those whose Q has been asked for
+        bool ok = true;
+        // lane 0 waits, the warp follows its verdict
+        auto wait = [&](uint64_t* bar, unsigned parity) -> bool {
+            const int got = lane != 0 || mbar_wait(bar, parity, abort_flag);
+            return __shfl_sync(0xffffffffu, got, 0) != 0;
+        };
+        for (; ok && !w.done(); w.next(a.s, a.Hkv, tt), ++li) {
+            const int n_qt = w.two(tt) ? 2 : 1;
+            if (li > 0 && !(ok = wait(&bars->q_empty, (li - 1) & 1))) break;
+            if (lane == 0) {
+                if (!w.whole()) {
+                    PagedPart& p = a.parts[2 * blockIdx.x + (w.first ? 0 : 1)];
+                    p.b = w.b;
+                    p.h = w.h;
+                    p.i = w.i;
+                    p.t0 = w.t0;
+                    p.t1 = w.t1;
+                    p.n_kv = w.n_kv;
+                }
+                mbar_arrive_expect_tx(&bars->q_full, (unsigned)(n_qt * G * tt * D * 2));
+                for (int t = 0; t < n_qt; ++t)
+                    for (int x = 0; x < kHalves; ++x)
+                        tma_load_3d(sQ + t * C::kQBytes + x * C::kBoxBytes, &tm_q, &bars->q_full, x * 64, w.h * G,
+                                    w.sq.q0 + (2 * w.i + t) * tt);
+            }
+            q_asked = li + 1;
+            for (int j = w.t0; ok && j < w.t1; ++j) {
+                // the lane's page, looked up while the stage drains
+                const int key = j * kTile + my_row;
+                int z = outside;
+                if (mine && key < w.sq.L) z = load_page(a.s, w.b, key >> shift) * a.Hkv + w.h;
+                const int y = key & ((1 << shift) - 1);
+#pragma unroll
+                for (int v = 0; v < 2; ++v, ++c_glob) {
+                    const int s = c_glob % C::kStages;
+                    if (c_glob >= C::kStages && !(ok = wait(&bars->empty[s], ((c_glob / C::kStages) - 1) & 1))) break;
+                    if (lane == 0) mbar_arrive_expect_tx(&bars->full[s], C::kTileBytes);
+                    __syncwarp();
+                    if (mine)
+                        tma_load_3d(sRing + s * C::kTileBytes + my_half * C::kBoxBytes + my_row * 128,
+                                    v ? &tm_v : &tm_k, &bars->full[s], my_half * 64, y, z);
+                    __syncwarp();
+                }
+            }
+        }
+        // never leave with copies in flight
+        for (int c = (c_glob > C::kStages ? c_glob - C::kStages : 0); c < c_glob; ++c)
+            mbar_wait(&bars->full[c % C::kStages], (c / C::kStages) & 1, nullptr);
+        if (q_asked > 0) mbar_wait(&bars->q_full, (q_asked - 1) & 1, nullptr);
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            // scale < 0: S is formed as (-Q) K^T and the softmax uses |scale|
+            const unsigned idesc_s = make_idesc_bf16(128, kTile, 0, 0) | (a.scale < 0.f ? kIdescNegateA : 0u);
+            constexpr unsigned idesc_o = make_idesc_bf16(128, D, 0, 1);
+            const uint32_t q_lo0 = desc_lo_kmajor(smem_u32(sQ));
+            const uint32_t q_lo1 = desc_lo_kmajor(smem_u32(sQ + C::kQBytes));
+            const uint32_t ring_k_lo = desc_lo_kmajor(smem_u32(sRing));
+            const uint32_t ring_v_lo = desc_lo_mnmajor(smem_u32(sRing));
+            constexpr uint32_t kStageStep = C::kTileBytes >> 4;
+            const unsigned tS0 = tmem, tS1 = tmem + 128u, tO0 = tmem + 256u, tO1 = tmem + 384u;
+            int stage = 0;
+            unsigned phase = 0;
+            auto next_tile = [&](uint32_t& off, int& st_used) -> bool {
+                if (!mbar_wait(&bars->full[stage], phase, abort_flag)) return false;
+                off = (uint32_t)stage * kStageStep;
+                st_used = stage;
+                if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
+                return true;
+            };
+            auto issue_s = [&](unsigned tS, uint32_t q_lo, uint32_t k_off) {
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    mma_ss_lo(tS, q_lo + kmajor_step(kk), ring_k_lo + k_off + kmajor_step(kk), idesc_s, kk > 0);
+            };
+            auto pv_halves = [&](int t, unsigned parity, uint32_t v_off, unsigned acc0) -> bool {
+                const unsigned tO = t ? tO1 : tO0, tS = t ? tS1 : tS0;
+                if (!mbar_wait(&bars->p_half[t], parity, abort_flag)) return false;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < kTile / 32; ++kk)
+                    mma_ts_lo(tO, tS + kk * 8, ring_v_lo + v_off + mnmajor_step(kk), idesc_o, (acc0 | kk) ? 1u : 0u);
+                if (!mbar_wait(&bars->p_ready[t], parity, abort_flag)) return false;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = kTile / 32; kk < kTile / 16; ++kk)
+                    mma_ts_lo(tO, tS + kk * 8, ring_v_lo + v_off + mnmajor_step(kk), idesc_o, 1u);
+                return true;
+            };
+            bool ok = true, prev_single = false;
+            int cnt0 = 0, cnt1 = 0;   // key tiles completed by each slot: phase of s_full / p_half / p_ready
+            int li = 0;
+            for (; ok && !w.done(); w.next(a.s, a.Hkv, tt), ++li) {
+                const bool single = !w.two(tt);
+                const int n1 = w.t1 - w.t0;
+                // A slot's first P V overwrites its O.  Its own epilogue of the
+                // item before is over when its softmax hands over P; after a
+                // single item the other slot's epilogue has read it as well.
+                auto o_is_free = [&](int t) -> bool {
+                    return !prev_single || mbar_wait(&bars->o_free[t ^ 1], (li - 1) & 1, abort_flag);
+                };
+                if (!(ok = mbar_wait(&bars->q_full, li & 1, abort_flag))) break;
+                uint32_t k_off = 0;
+                int k_stage = 0;
+                if (single) {
+                    uint32_t v_off0 = 0, v_off1 = 0;
+                    int v_stage0 = 0, v_stage1 = 0;
+                    for (int t = 0; ok && t < 2 && t < n1; ++t) {
+                        if (!(ok = next_tile(k_off, k_stage))) break;
+                        tc_fence_after();
+                        issue_s(t ? tS1 : tS0, q_lo0, k_off);
+                        mma_commit(&bars->s_full[t]);
+                        mma_commit(&bars->empty[k_stage]);
+                        if (t + 1 == n1) mma_commit(&bars->q_empty);   // Q read by its last S
+                        ok = t ? next_tile(v_off1, v_stage1) : next_tile(v_off0, v_stage0);
+                    }
+                    for (int j = 0; ok && j < n1; ++j) {
+                        const int t = j & 1;
+                        if (j < 2 && !(ok = o_is_free(t))) break;
+                        if (!(ok = pv_halves(t, (t ? cnt1 : cnt0) & 1, t ? v_off1 : v_off0, j >= 2 ? 1u : 0u))) break;
+                        if (t) ++cnt1; else ++cnt0;
+                        mma_commit(&bars->empty[t ? v_stage1 : v_stage0]);
+                        if (j + 2 < n1) {
+                            if (!(ok = next_tile(k_off, k_stage))) break;
+                            tc_fence_after();
+                            issue_s(t ? tS1 : tS0, q_lo0, k_off);
+                            mma_commit(&bars->s_full[t]);
+                            mma_commit(&bars->empty[k_stage]);
+                            if (j + 3 == n1) mma_commit(&bars->q_empty);
+                            ok = t ? next_tile(v_off1, v_stage1) : next_tile(v_off0, v_stage0);
+                        }
+                    }
+                } else {
+                    const int n0 = w.tiles_slot0(tt);   // <= n1
+                    if (!(ok = next_tile(k_off, k_stage))) break;
+                    tc_fence_after();
+                    if (n0 > 0) {
+                        issue_s(tS0, q_lo0, k_off);
+                        mma_commit(&bars->s_full[0]);
+                    }
+                    issue_s(tS1, q_lo1, k_off);
+                    mma_commit(&bars->s_full[1]);
+                    mma_commit(&bars->empty[k_stage]);
+                    if (n1 == 1) mma_commit(&bars->q_empty);
+                    for (int j = 0; ok && j < n1; ++j) {
+                        const bool more = j + 1 < n1;
+                        const unsigned acc0 = j > 0 ? 1u : 0u;
+                        uint32_t v_off = 0;
+                        int v_stage = 0;
+                        if (!(ok = next_tile(v_off, v_stage))) break;
+                        if (j < n0) {
+                            if (j == 0 && !(ok = o_is_free(0))) break;
+                            if (!(ok = pv_halves(0, cnt0 & 1, v_off, acc0))) break;
+                            ++cnt0;
+                        }
+                        if (more) {
+                            if (!(ok = next_tile(k_off, k_stage))) break;
+                            tc_fence_after();
+                            if (j + 1 < n0) {
+                                issue_s(tS0, q_lo0, k_off);
+                                mma_commit(&bars->s_full[0]);
+                            }
+                        }
+                        if (j == 0 && !(ok = o_is_free(1))) break;
+                        if (!(ok = pv_halves(1, cnt1 & 1, v_off, acc0))) break;
+                        ++cnt1;
+                        mma_commit(&bars->empty[v_stage]);
+                        if (more) {
+                            issue_s(tS1, q_lo1, k_off);
+                            mma_commit(&bars->s_full[1]);
+                            mma_commit(&bars->empty[k_stage]);
+                            if (j + 2 == n1) mma_commit(&bars->q_empty);
+                        }
+                    }
+                }
+                // No slot may fall a whole phase of o_final behind (one with no
+                // key tiles in an item waits for nothing else): both have
+                // finished the item before.
+                if (ok && li > 0)
+                    ok = mbar_wait(&bars->o_free[0], (li - 1) & 1, abort_flag) &&
+                         mbar_wait(&bars->o_free[1], (li - 1) & 1, abort_flag);
+                if (ok) mma_commit(&bars->o_final);
+                prev_single = single;
+            }
+            mma_commit(&bars->drain);
+            mbar_wait(&bars->drain, 0, nullptr);
+        }
+    } else {
+        // ------------------------------------------------ softmax / epilogue
+        const int t = (warp - 2) >> 2;
+        const unsigned sub = warp & 3;
+        const int r = (int)sub * 32 + (int)lane;
+        const unsigned lane_off = (sub * 32u) << 16;
+        const unsigned tS = tmem + lane_off + (t ? 128u : 0u);
+        const unsigned tO = tmem + lane_off + (t ? 384u : 256u);
+        // S carries the sign; a scale of 0 must not meet the mask's infinity
+        const float c_log2 = fmaxf(fabsf(a.scale) * kLog2e, 1e-37f);
+        const int tok_r = r / G;               // token of row r in its query tile
+        const int g_r = r - tok_r * G;
+        const int page = 1 << a.s.page_shift;
+        bool ok = true;
+        int kt = 0;         // key tiles completed by this slot (all items)
+        int ring = 0;       // ring tiles in front of the current item
+        int n_single = 0;   // single items completed by this CTA
+        int li = 0;
+        for (; ok && !w.done(); w.next(a.s, a.Hkv, tt), ++li) {
+            const bool single = !w.two(tt);
+            const int cnt = w.t1 - w.t0;
+            const int n0 = single ? 0 : w.tiles_slot0(tt);
+            // a two-tile item's slot t owns query tile t; a single item's slots
+            // own its one tile and key tiles t, t+2, ...
+            const int n_mine = single ? (cnt + 1 - t) / 2 : (t ? cnt : n0);
+            const int tok0 = (2 * w.i + (single ? 0 : t)) * tt;
+            const bool valid = tok_r < tt && tok0 + tok_r < w.sq.n;
+            const bool live = __any_sync(0xffffffffu, valid);   // rows of other lanes never meet this warp's
+            // keys the row sees, from the item's first key tile on
+            const int lim = max(0, w.sq.L - w.sq.n + min(tok0 + tok_r, w.sq.n - 1) + 1) - w.t0 * kTile;
+            const int len = w.sq.L - w.t0 * kTile;               // keys of the sequence, likewise
+            float m_ref = kNoKey;
+            float l = 0.f;
+            for (int it = 0; it < n_mine; ++it, ++kt) {
+                const int j = single ? 2 * it + t : it;          // key tile of this share of the item
+                if (!(ok = mbar_wait(&bars->s_full[t], kt & 1, abort_flag))) break;
+                tc_fence_after();
+                // values behind the sequence's last key: zeros, before any P V reads the tile
+                const int nv = len - j * kTile;
+                if (nv < kTile && nv > 0 && nv % page != 0 && (single || t == 0 || j >= n0)) {
+                    const int c = ring + 2 * j + 1;
+                    const int s = c % C::kStages;
+                    if (!(ok = mbar_wait(&bars->full[s], (c / C::kStages) & 1, abort_flag))) break;
+                    const int stop = min(kTile, (nv + page - 1) / page * page);
+                    uint8_t* tile = sRing + s * C::kTileBytes;
+                    const int chunks = (stop - nv) * 8;           // 16-byte pieces of one box
+                    for (int e = r; e < chunks * (D / 64); e += 128) {
+                        const int x = e / chunks;
+                        *reinterpret_cast<uint4*>(tile + x * C::kBoxBytes + nv * 128 + (e - x * chunks) * 16) =
+                            make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                }
+                if (!live) {
+                    mbar_arrive(&bars->p_half[t]);
+                    mbar_arrive(&bars->p_ready[t]);
+                    continue;
+                }
+                uint32_t sr[kTile];
+#pragma unroll
+                for (int c0 = 0; c0 < kTile; c0 += 32) tmem_ld32(tS + c0, *reinterpret_cast<uint32_t(*)[32]>(&sr[c0]));
+                tmem_wait_ld();
+                const int nvalid = lim - j * kTile;
+                if (nvalid < kTile) {
+#pragma unroll
+                    for (int c = 0; c < kTile; ++c)
+                        if (c >= nvalid) sr[c] = __float_as_uint(-INFINITY);
+                }
+                float mxa[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) mxa[i] = fmaxf(__uint_as_float(sr[i]), __uint_as_float(sr[8 + i]));
+#pragma unroll
+                for (int c = 16; c < kTile; c += 16)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        mxa[i] = fmax3(mxa[i], __uint_as_float(sr[c + i]), __uint_as_float(sr[c + 8 + i]));
+                const float mx = fmaxf(fmax3(mxa[0], mxa[1], mxa[2]), fmax3(fmax3(mxa[3], mxa[4], mxa[5]), mxa[6], mxa[7]));
+                const float m_blk = fmaxf(mx * c_log2, kNoKey);
+                float alpha = 1.f;
+                bool rescale = false;
+                if (it == 0) {
+                    m_ref = m_blk;
+                } else if (__any_sync(0xffffffffu, m_blk - m_ref > kRescaleThreshold)) {
+                    const float m_new = fmaxf(m_ref, m_blk);
+                    alpha = ex2_approx(m_ref - m_new);
+                    m_ref = m_new;
+                    rescale = true;
+                }
+                l *= alpha;
+                float rsa[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) rsa[i] = 0.f;
+#pragma unroll
+                for (int c0 = 0; c0 < kTile; c0 += 32) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int c = 0; c < 32; c += 2) {
+                        const float p0 = ex2_approx(fmaf(__uint_as_float(sr[c0 + c]), c_log2, -m_ref));
+                        const float p1 = ex2_approx(fmaf(__uint_as_float(sr[c0 + c + 1]), c_log2, -m_ref));
+                        rsa[(c / 2) & 7] += p0 + p1;
+                        pk[c / 2] = pack_bf16x2(p0, p1);
+                    }
+                    tmem_st16(tS + c0 / 2, pk);
+                    if (c0 == kTile / 2 - 32 && !rescale) {
+                        tmem_wait_st();
+                        tc_fence_before();
+                        mbar_arrive(&bars->p_half[t]);
+                    }
+                }
+                l += ((rsa[0] + rsa[1]) + (rsa[2] + rsa[3])) + ((rsa[4] + rsa[5]) + (rsa[6] + rsa[7]));
+                if (rescale) {
+                    // P V of this slot's previous key tile has completed (it was
+                    // issued before S of this one, whose commit was waited on)
+#pragma unroll
+                    for (int c0 = 0; c0 < D; c0 += 32) {
+                        uint32_t ov[32];
+                        tmem_ld32(tO + c0, ov);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+                        tmem_st32(tO + c0, ov);
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                if (rescale) mbar_arrive(&bars->p_half[t]);
+                mbar_arrive(&bars->p_ready[t]);
+            }
+            if (!ok) break;
+            ring += 2 * cnt;
+            // A single item's slots fold their summaries of the same rows and
+            // each writes half of the head dims, reading both slots' O (slot 1
+            // has none when the share has one key tile).
+            const bool with1 = single && cnt >= 2;
+            float w0 = 1.f, w1 = 0.f, M = m_ref, L = l;
+            if (single) {
+                // the other slot has read the previous item's summaries
+                if (li > 0 && !(ok = mbar_wait(&bars->o_free[t ^ 1], (li - 1) & 1, abort_flag))) break;
+                sMerge[2 * (t * kTile + r)] = m_ref;
+                sMerge[2 * (t * kTile + r) + 1] = l;
+                mbar_arrive(&bars->merge_ready);
+                if (!(ok = mbar_wait(&bars->merge_ready, n_single & 1, abort_flag))) break;
+                ++n_single;
+                const float m_o = sMerge[2 * ((t ^ 1) * kTile + r)];
+                const float l_o = sMerge[2 * ((t ^ 1) * kTile + r) + 1];
+                M = fmaxf(m_ref, m_o);
+                const float w_self = ex2_approx(m_ref - M), w_oth = ex2_approx(m_o - M);
+                L = w_self * l + w_oth * l_o;
+                w0 = t ? w_oth : w_self;
+                w1 = t ? w_self : w_oth;
+            }
+            if (!(ok = mbar_wait(&bars->o_final, li & 1, abort_flag))) break;
+            tc_fence_after();
+            if (live) {
+                const bool whole = w.whole();
+                const bool none = L == 0.f;     // no key in sight: O may never have been written
+                const float inv = none ? 0.f : whole ? 1.f / L : 1.f;
+                const float s0 = w0 * inv, s1 = w1 * inv;
+                const int c_begin = single ? t * (D / 2) : 0;
+                const int n_chunks = single ? D / 32 : D / 16;
+                const unsigned tOa = single ? tmem + lane_off + 256u : tO;
+                const unsigned tOb = tmem + lane_off + 384u;
+                const size_t orow = (size_t)(w.sq.q0 + tok0 + tok_r) * a.H + w.h * G + g_r;
+                const int prow = (2 * (int)blockIdx.x + (w.first ? 0 : 1)) * 2 * tt * G + (single ? 0 : t * tt * G) + r;
+                uint16_t* out = static_cast<uint16_t*>(a.o) + orow * D;
+                float* part = a.part_acc + (size_t)prow * D;
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    if (k >= n_chunks) break;
+                    const int c0 = c_begin + 16 * k;
+                    uint32_t x[16];
+                    float f[16];
+                    tmem_ld16(tOa + c0, x);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) f[i] = none ? 0.f : __uint_as_float(x[i]) * s0;
+                    if (with1) {
+                        tmem_ld16(tOb + c0, x);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) f[i] = none ? 0.f : fmaf(__uint_as_float(x[i]), s1, f[i]);
+                    }
+                    if (!valid) continue;
+                    if (whole) {
+                        uint32_t packed[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) packed[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+                        uint4* dst = reinterpret_cast<uint4*>(out + c0);
+                        dst[0] = make_uint4(packed[0], packed[1], packed[2], packed[3]);
+                        dst[1] = make_uint4(packed[4], packed[5], packed[6], packed[7]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; i += 4)
+                            *reinterpret_cast<float4*>(part + c0 + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+                    }
+                }
+                if (valid && (!single || t == 0)) {
+                    if (whole)
+                        a.lse[orow] = none ? -INFINITY : (M + __log2f(L)) * kLn2;
+                    else
+                        *reinterpret_cast<float2*>(a.part_ml + 2 * (size_t)prow) =
+                            make_float2(none ? -INFINITY : M, L);
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(&bars->o_free[t]);
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// Joins the parts of the item that CTA blockIdx.x of the main kernel began and
+// did not finish: the first in one of its own slots, the others in the first
+// slots of the CTAs behind it.  grid.y: slices of the item's rows; a warp takes
+// a row, a lane D / 32 head dims.
+constexpr int kMergeThreads = 256;
+constexpr int kMergeRows = 32;    // rows per CTA
+constexpr int kMergeBatch = 4;
+
+template <int DPL>
+__global__ void __launch_bounds__(kMergeThreads) paged_tc_merge_kernel(const PagedTcArgs a, int ctas) {
+    constexpr int D = 32 * DPL;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int c0 = (int)blockIdx.x;
+    int slot = 2 * c0;
+    PagedPart p = a.parts[slot];
+    if (p.n_kv == 0 || p.t0 != 0) p = a.parts[++slot];
+    if (p.n_kv == 0 || p.t0 != 0) return;
+    int c1 = c0;                       // last CTA with a part
+    {
+        PagedPart e = p;
+        while (e.t1 < p.n_kv && c1 + 1 < ctas) {
+            const PagedPart n = a.parts[2 * ++c1];
+            if (n.n_kv != 0) e = n;   // with fewer tiles than CTAs some have no share
+        }
+    }
+    const Seq sq = load_seq(a.s, p.b);
+    const int G = a.H / a.Hkv;
+    const int rows = 2 * a.tt * G;
+    const int warp = (int)warp_id(), lane = (int)lane_id();
+    for (int r = (int)blockIdx.y * kMergeRows + warp; r < min(rows, ((int)blockIdx.y + 1) * kMergeRows);
+         r += kMergeThreads / 32) {
+        const int tok = p.i * 2 * a.tt + r / G;
+        if (tok >= sq.n) break;
+        float M = -INFINITY, L = 0.f, A[DPL];
+#pragma unroll
+        for (int i = 0; i < DPL; ++i) A[i] = 0.f;
+        for (int c = c0; c <= c1; c += kMergeBatch) {
+            float mc[kMergeBatch], lc[kMergeBatch], x[kMergeBatch][DPL];
+#pragma unroll
+            for (int u = 0; u < kMergeBatch; ++u) {
+                mc[u] = -INFINITY;
+                if (c + u <= c1 && (c + u == c0 || a.parts[2 * (c + u)].n_kv != 0)) {
+                    const size_t row = (size_t)(c + u == c0 ? slot : 2 * (c + u)) * rows + r;
+                    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + 2 * row);
+                    mc[u] = ml.x;
+                    lc[u] = ml.y;
+                    load_row(a.part_acc + row * D + lane * DPL, x[u]);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kMergeBatch; ++u) {
+                if (mc[u] == -INFINITY) continue;
+                const float mn = fmaxf(M, mc[u]);
+                const float al = ex2_approx(M - mn);   // 0 while M = -inf
+                const float wc = ex2_approx(mc[u] - mn);
+                M = mn;
+                L = fmaf(wc, lc[u], L * al);
+#pragma unroll
+                for (int i = 0; i < DPL; ++i) A[i] = fmaf(wc, x[u][i], A[i] * al);
+            }
+        }
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        const size_t row = (size_t)(sq.q0 + tok) * a.H + p.h * G + r % G;
+        uint16_t* out = static_cast<uint16_t*>(a.o) + row * D + lane * DPL;
+#pragma unroll
+        for (int i = 0; i < DPL; i += 2)
+            *reinterpret_cast<uint32_t*>(out + i) = pack_bf16x2(A[i] * inv, A[i + 1] * inv);
+        if (lane == 0) a.lse[row] = L == 0.f ? -INFINITY : (M + __log2f(L)) * kLn2;
+    }
+}
+
+template <int D>
+cudaError_t launch_d(const PagedTcArgs& a, int sm_count, cudaStream_t stream) {
+    using C = Cfg<D>;
+    auto kern = paged_tc_kernel<D>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)sm_count);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = C::kSmemBytes;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if ((e = cudaLaunchKernelEx(&cfg, kern, a.tm_q, a.tm_k, a.tm_v, a)) != cudaSuccess) return e;
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    const int rows = 2 * a.tt * (a.H / a.Hkv);
+    cfg.gridDim = dim3((unsigned)sm_count, (unsigned)((rows + kMergeRows - 1) / kMergeRows));
+    cfg.blockDim = dim3(kMergeThreads);
+    cfg.dynamicSmemBytes = 0;
+    if ((e = cudaLaunchKernelEx(&cfg, paged_tc_merge_kernel<D / 32>, a, sm_count)) != cudaSuccess) return e;
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+int paged_tc_tokens(int G, int max_q) {
+    if (G > kTile) return 0;
+    const int most = kTile / G;
+    return max_q >= 1 && max_q < most ? max_q : most;
+}
+
+cudaError_t launch_paged_tc(const PagedTcArgs& a, int sm_count, cudaStream_t stream) {
+    return a.D == 64 ? launch_d<64>(a, sm_count, stream) : launch_d<128>(a, sm_count, stream);
+}
+
+}  // namespace mea
