@@ -42,6 +42,7 @@ __all__ = [
     "MEA_ROPE_HALF", "MEA_ROPE_INTERLEAVED", "MEA_ROPE_SCALE_NONE", "MEA_ROPE_SCALE_LINEAR", "MEA_ROPE_SCALE_BASE",
     "MEA_ROPE_SCALE_BY_PARTS", "mea_rope_frequencies", "mea_rope", "rope", "mea_paged_append", "paged_append",
     "mea_attn_paged", "mea_attn_paged_workspace_size", "attention_paged", "mea_attn_paged_weights",
+    "mea_attn_paged_weights_workspace_size",
     "attention_paged_weights", "mea_paged_evict", "paged_evict",
     "mea_last_device_error",
     "mea_selftest_bounded_wait", "mea_status_string", "mea_last_error_message", "mea_version", "attention_forward", "attention_backward",
@@ -144,7 +145,9 @@ def load_library() -> ctypes.CDLL:
     lib.mea_attn_paged_workspace_size.restype = i
     lib.mea_attn_paged.argtypes = [vp] * 8 + [i] * 5 + [ll] + [i] * 5 + [f, i, vp, sz, vp]
     lib.mea_attn_paged.restype = i
-    lib.mea_attn_paged_weights.argtypes = [vp] * 7 + [i] * 5 + [ll] + [i] * 5 + [f, i, vp]
+    lib.mea_attn_paged_weights_workspace_size.argtypes = [i] * 8 + [ctypes.POINTER(sz)]
+    lib.mea_attn_paged_weights_workspace_size.restype = i
+    lib.mea_attn_paged_weights.argtypes = [vp] * 7 + [i] * 5 + [ll] + [i] * 5 + [f, i, vp, sz, vp]
     lib.mea_attn_paged_weights.restype = i
     lib.mea_paged_evict.argtypes = [vp] * 8 + [i] * 9 + [i, vp]
     lib.mea_paged_evict.restype = i
@@ -526,11 +529,8 @@ def _batch(where: str, kv_len, page_table, cu_q=None):
 
 
 def _launch(where: str, fn, device, stream, *args) -> None:
-    """fn(*args, stream) with ``device`` current (its own stream where none is given)."""
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            st = fn(*args, _stream_handle(stream))
-    else:
+    """fn(*args, stream) with ``device`` current (its current stream where none is given)."""
+    with _on(device):
         st = fn(*args, _stream_handle(stream))
     _check(st, where)
 
@@ -619,14 +619,38 @@ def paged_append(q, k, v, k_cache, v_cache, weights, cu_q, kv_len, page_table, p
     return q_out
 
 
+def _paged_workspace(where: str, fn, sizes, dtype) -> int:
+    out = ctypes.c_size_t(0)
+    _check(fn(*sizes, MEA_DTYPE_BF16 if dtype == torch.bfloat16 else MEA_DTYPE_F32, ctypes.byref(out)), where)
+    return int(out.value)
+
+
 def mea_attn_paged_workspace_size(T: int, B: int, H: int, H_kv: int, D: int, max_q: int, max_kv: int,
                                   dtype=torch.bfloat16) -> int:
     """C ``mea_attn_paged_workspace_size`` (for the current CUDA device)."""
-    out = ctypes.c_size_t(0)
-    code = MEA_DTYPE_BF16 if dtype == torch.bfloat16 else MEA_DTYPE_F32
-    _check(load_library().mea_attn_paged_workspace_size(T, B, H, H_kv, D, max_q, max_kv, code, ctypes.byref(out)),
-           "mea_attn_paged_workspace_size")
-    return int(out.value)
+    return _paged_workspace("mea_attn_paged_workspace_size", load_library().mea_attn_paged_workspace_size,
+                            (T, B, H, H_kv, D, max_q, max_kv), dtype)
+
+
+def mea_attn_paged_weights_workspace_size(T: int, B: int, H: int, H_kv: int, D: int, max_q: int, max_kv: int,
+                                          dtype=torch.bfloat16) -> int:
+    """C ``mea_attn_paged_weights_workspace_size`` (for the current CUDA device)."""
+    return _paged_workspace("mea_attn_paged_weights_workspace_size",
+                            load_library().mea_attn_paged_weights_workspace_size,
+                            (T, B, H, H_kv, D, max_q, max_kv), dtype)
+
+
+def _on(device):
+    """Context with ``device`` current (nothing to do where it is)."""
+    return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+def _workspace_bytes(where: str, workspace, device) -> int:
+    if workspace is None:
+        return 0
+    if workspace.device != device or not workspace.is_contiguous():
+        _bad(where, "workspace must be a contiguous tensor on the device")
+    return workspace.numel() * workspace.element_size()
 
 
 def mea_attn_paged(q, k_cache, v_cache, o, lse, cu_q, kv_len, page_table, max_q: int, max_kv: int, scale: float,
@@ -644,11 +668,7 @@ def mea_attn_paged(q, k_cache, v_cache, o, lse, cu_q, kv_len, page_table, max_q:
     _same_device(w, q, (("k_cache", k_cache, dt), ("v_cache", v_cache, dt), ("o", o, dt), ("lse", lse, torch.float32),
                         ("cu_q", cu_q, torch.int32), ("kv_len", kv_len, torch.int32),
                         ("page_table", page_table, torch.int32)))
-    ws_bytes = 0
-    if workspace is not None:
-        if workspace.device != q.device or not workspace.is_contiguous():
-            _bad(w, "workspace must be a contiguous tensor on the device")
-        ws_bytes = workspace.numel() * workspace.element_size()
+    ws_bytes = _workspace_bytes(w, workspace, q.device)
     _launch(w, load_library().mea_attn_paged, q.device, stream, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(o),
             _ptr(lse), _ptr(cu_q), _ptr(kv_len), _ptr(page_table), T, B, H, Hkv, D, qs, pages, page, max_pages,
             int(max_q), int(max_kv), float(scale), _dtype_code(q), _ptr(workspace), ws_bytes)
@@ -666,7 +686,7 @@ def attention_paged(q, k_cache, v_cache, cu_q, kv_len, page_table, max_q: int, m
     if scale is None:
         scale = 1.0 / math.sqrt(q.shape[-1])
     T, H, D = q.shape
-    with torch.cuda.device(q.device) if q.device.index != torch.cuda.current_device() else contextlib.nullcontext():
+    with _on(q.device):
         n = mea_attn_paged_workspace_size(T, kv_len.shape[0], H, k_cache.shape[1], D, max_q, max_kv, q.dtype)
     with _allocating(stream, q.device):
         o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
@@ -677,9 +697,10 @@ def attention_paged(q, k_cache, v_cache, cu_q, kv_len, page_table, max_q: int, m
 
 
 def mea_attn_paged_weights(q, lse, k_cache, weights, cu_q, kv_len, page_table, max_q: int, max_kv: int, scale: float,
-                           stream=None) -> None:
+                           workspace=None, stream=None) -> None:
     """C ``mea_attn_paged_weights``: adds to weights [pages,H_kv,page_size] what every cached key's
-    probabilities sum to over the rows of the call (lse [T,H] from ``mea_attn_paged``)."""
+    probabilities sum to over the rows of the call (lse [T,H] from ``mea_attn_paged``).  ``workspace`` of
+    ``mea_attn_paged_weights_workspace_size`` bytes (None when 0)."""
     w = "mea_attn_paged_weights"
     pages, Hkv, page, D = _pages(w, k_cache, None, weights, q)
     B, max_pages = _batch(w, kv_len, page_table, cu_q)
@@ -692,14 +713,25 @@ def mea_attn_paged_weights(q, lse, k_cache, weights, cu_q, kv_len, page_table, m
                         ("page_table", page_table, torch.int32)))
     _launch(w, load_library().mea_attn_paged_weights, q.device, stream, _ptr(q), _ptr(lse), _ptr(k_cache),
             _ptr(weights), _ptr(cu_q), _ptr(kv_len), _ptr(page_table), T, B, H, Hkv, D, qs, pages, page, max_pages,
-            int(max_q), int(max_kv), float(scale), _dtype_code(q))
+            int(max_q), int(max_kv), float(scale), _dtype_code(q), _ptr(workspace),
+            _workspace_bytes(w, workspace, q.device))
 
 
 def attention_paged_weights(q, lse, k_cache, weights, cu_q, kv_len, page_table, max_q: int, max_kv: int,
                             scale: float | None = None, stream=None) -> None:
-    """``mea_attn_paged_weights`` with the scale of ``attention_paged``."""
+    """Allocate the workspace with torch and run ``mea_attn_paged_weights``."""
+    _pages("attention_paged_weights", k_cache, None, weights)
+    if q.dim() != 3:
+        _bad("attention_paged_weights", "q must be [T, H, D]")
+    if not q.is_cuda:
+        _bad("attention_paged_weights", "CUDA tensors")
+    T, H, D = q.shape
+    with _on(q.device):
+        n = mea_attn_paged_weights_workspace_size(T, kv_len.shape[0], H, k_cache.shape[1], D, max_q, max_kv, q.dtype)
+    with _allocating(stream, q.device):
+        ws = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
     mea_attn_paged_weights(q, lse, k_cache, weights, cu_q, kv_len, page_table, max_q, max_kv,
-                           1.0 / math.sqrt(q.shape[-1]) if scale is None else scale, stream)
+                           1.0 / math.sqrt(D) if scale is None else scale, ws, stream)
 
 
 def mea_paged_evict(k_cache, v_cache, weights, page_table, kv_len, dst_table, kv_len_out, keep_idx, n_recent: int,

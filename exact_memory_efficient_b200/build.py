@@ -26,7 +26,7 @@ LIB_NAME = "libmea_attn.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 
 SOURCES = ["api.cu", "fwd_f32.cu", "bwd_f32.cu", "fwd_bf16.cu", "fwd_persist.cu", "bwd_bf16.cu", "combine.cu", "decode.cu",
-           "api_paged.cu", "rope.cu", "paged_attn.cu", "paged_tc.cu", "paged_weights.cu", "paged_evict.cu"]
+           "api_paged.cu", "rope.cu", "paged_attn.cu", "paged_tc.cu", "paged_weights.cu", "paged_weights_tc.cu", "paged_evict.cu"]
 HEADERS = ["ptx.cuh", "kernels.h", "simt_f32.cuh", "rows.cuh", "paged.cuh", "api_internal.h"]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]

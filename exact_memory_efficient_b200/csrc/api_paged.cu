@@ -107,6 +107,35 @@ AttnPlan attn_plan(int sm_count, int T, int B, int H, int H_kv, int D, int max_q
     return p;
 }
 
+// Maps of packed q (boxes of tt tokens of one group) and of a cache's pages.
+mea_status_t map_q(CUtensorMap* m, const void* q, int T, int H, int G, int D, long long q_stride, int tt) {
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)T};
+    const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)q_stride * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)tt};
+    return mea::api_map_bf16(m, q, dims, strides, box, "q");
+}
+mea_status_t map_pages(CUtensorMap* m, const void* cache, int num_pages, int H_kv, int page_size, int D) {
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)page_size, (cuuint64_t)num_pages * H_kv};
+    const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)page_size * D * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)std::min(page_size, 128), 1};
+    return mea::api_map_bf16(m, cache, dims, strides, box, "cache");
+}
+
+struct WeightsPlan {
+    int tt = 0;                // 0: the CUDA-core kernel
+    bool split = false;
+    size_t ws_bytes = 0;
+};
+// Where one query tile holds all new tokens of a sequence an item has one unit
+// and nothing to split.
+WeightsPlan weights_plan(int sm_count, int G, int max_q, bool bf16) {
+    WeightsPlan p;
+    if (!bf16 || (p.tt = mea::paged_tc_tokens(G, max_q)) == 0) return p;
+    p.split = max_q > p.tt;
+    if (p.split) p.ws_bytes = (size_t)2 * sm_count * (mea::kWeightsPartKeys * sizeof(float) + sizeof(mea::PagedPart));
+    return p;
+}
+
 }  // namespace
 
 extern "C" {
@@ -277,16 +306,9 @@ mea_status_t mea_attn_paged(const void* q, const void* k_cache, const void* v_ca
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (p.tt > 0) {
         mea::PagedTcArgs t;
-        const int G = H / H_kv;
-        const cuuint64_t q_dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)T};
-        const cuuint64_t q_strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)q_stride * 2};
-        const cuuint32_t q_box[3] = {64, (cuuint32_t)G, (cuuint32_t)p.tt};
-        const cuuint64_t k_dims[3] = {(cuuint64_t)D, (cuuint64_t)page_size, (cuuint64_t)num_pages * H_kv};
-        const cuuint64_t k_strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)page_size * D * 2};
-        const cuuint32_t k_box[3] = {64, (cuuint32_t)std::min(page_size, 128), 1};
-        if ((st = mea::api_map_bf16(&t.tm_q, q, q_dims, q_strides, q_box, "q")) != MEA_OK) return st;
-        if ((st = mea::api_map_bf16(&t.tm_k, k_cache, k_dims, k_strides, k_box, "k_cache")) != MEA_OK) return st;
-        if ((st = mea::api_map_bf16(&t.tm_v, v_cache, k_dims, k_strides, k_box, "v_cache")) != MEA_OK) return st;
+        if ((st = map_q(&t.tm_q, q, T, H, H / H_kv, D, q_stride, p.tt)) != MEA_OK) return st;
+        if ((st = map_pages(&t.tm_k, k_cache, num_pages, H_kv, page_size, D)) != MEA_OK) return st;
+        if ((st = map_pages(&t.tm_v, v_cache, num_pages, H_kv, page_size, D)) != MEA_OK) return st;
         t.s = batch_of(cu_q, kv_len, page_table, T, B, num_pages, page_size, max_pages);
         t.o = o;
         t.lse = lse;
@@ -320,10 +342,27 @@ mea_status_t mea_attn_paged(const void* q, const void* k_cache, const void* v_ca
     return mea::api_cuda(mea::launch_paged_merge(a, bf16, s), where);
 }
 
+mea_status_t mea_attn_paged_weights_workspace_size(int T, int B, int H, int H_kv, int D, int max_q, int max_kv,
+                                                   mea_dtype_t dtype, size_t* bytes) {
+    const char* where = "mea_attn_paged_weights_workspace_size";
+    if (bytes == nullptr) return invalid(where, "null pointer");
+    mea_status_t st = check_batch(where, T, B, H_kv, D, 1, 16, 1, dtype);
+    if (st != MEA_OK) return st;
+    if ((st = check_heads(where, T, H, H_kv, D, (long long)H * D)) != MEA_OK) return st;
+    if (max_q < 0 || max_kv < 0) return invalid(where, "negative bound");
+    *bytes = 0;
+    if (T == 0 || B == 0) return MEA_OK;
+    int sms = 0;
+    if ((st = mea::api_device(&sms)) != MEA_OK) return st;
+    *bytes = weights_plan(sms, H / H_kv, max_q, dtype == MEA_DTYPE_BF16).ws_bytes;
+    return MEA_OK;
+}
+
 mea_status_t mea_attn_paged_weights(const void* q, const float* lse, const void* k_cache, float* weights,
                                     const int* cu_q, const int* kv_len, const int* page_table, int T, int B, int H,
                                     int H_kv, int D, long long q_stride, int num_pages, int page_size, int max_pages,
-                                    int max_q, int max_kv, float scale, mea_dtype_t dtype, void* stream) {
+                                    int max_q, int max_kv, float scale, mea_dtype_t dtype, void* workspace,
+                                    size_t workspace_bytes, void* stream) {
     const char* where = "mea_attn_paged_weights";
     mea_status_t st = check_batch(where, T, B, H_kv, D, num_pages, page_size, max_pages, dtype);
     if (st != MEA_OK) return st;
@@ -338,6 +377,30 @@ mea_status_t mea_attn_paged_weights(const void* q, const float* lse, const void*
         return MEA_ERR_MISALIGNED;
     int sms = 0;
     if ((st = mea::api_device(&sms)) != MEA_OK) return st;
+    const WeightsPlan p = weights_plan(sms, H / H_kv, max_q, dtype == MEA_DTYPE_BF16);
+    if (p.ws_bytes > 0) {
+        if (workspace == nullptr || workspace_bytes < p.ws_bytes)
+            return api_fail(MEA_ERR_WORKSPACE, where, "workspace missing or below mea_attn_paged_weights_workspace_size");
+        if (!aligned(workspace, 16)) return MEA_ERR_MISALIGNED;
+    }
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (p.tt > 0) {
+        mea::PagedWeightsTcArgs t;
+        if ((st = map_q(&t.tm_q, q, T, H, H / H_kv, D, q_stride, p.tt)) != MEA_OK) return st;
+        if ((st = map_pages(&t.tm_k, k_cache, num_pages, H_kv, page_size, D)) != MEA_OK) return st;
+        t.s = batch_of(cu_q, kv_len, page_table, T, B, num_pages, page_size, max_pages);
+        t.lse = lse;
+        t.weights = weights;
+        t.part_sum = static_cast<float*>(workspace);
+        t.parts = p.split ? reinterpret_cast<mea::PagedPart*>(t.part_sum + (size_t)2 * sms * mea::kWeightsPartKeys) : nullptr;
+        t.H = H;
+        t.Hkv = H_kv;
+        t.D = D;
+        t.tt = p.tt;
+        t.scale = scale;
+        t.split = p.split;
+        return mea::api_cuda(mea::launch_paged_weights_tc(t, sms, s), where);
+    }
     mea::PagedWeightsArgs a;
     a.s = batch_of(cu_q, kv_len, page_table, T, B, num_pages, page_size, max_pages);
     a.q = q;
@@ -350,7 +413,7 @@ mea_status_t mea_attn_paged_weights(const void* q, const float* lse, const void*
     a.D = D;
     a.max_kv = max_kv;
     a.scale = scale;
-    return mea::api_cuda(mea::launch_paged_weights_simt(a, dtype == MEA_DTYPE_BF16, static_cast<cudaStream_t>(stream)), where);
+    return mea::api_cuda(mea::launch_paged_weights_simt(a, dtype == MEA_DTYPE_BF16, s), where);
 }
 
 mea_status_t mea_paged_evict(void* k_cache, void* v_cache, float* weights, const int* page_table, const int* kv_len,

@@ -251,6 +251,22 @@ struct PagedWeightsArgs {
 };
 cudaError_t launch_paged_weights_simt(const PagedWeightsArgs& a, bool bf16, cudaStream_t stream);
 
+// The same on the tensor cores (paged_weights_tc.cu), bf16; maps as for
+// PagedTcArgs.  split: workspace part_sum [2 sm_count, 256] and parts [2 sm_count].
+struct PagedWeightsTcArgs {
+    CUtensorMap tm_q, tm_k;
+    PagedBatch s;
+    const float* lse;
+    float* weights;
+    float* part_sum;
+    PagedPart* parts;          // i: 256-key item; t0, t1, n_kv: its query tiles
+    int H, Hkv, D, tt;
+    float scale;
+    bool split;
+};
+constexpr int kWeightsPartKeys = 256;
+cudaError_t launch_paged_weights_tc(const PagedWeightsTcArgs& a, int sm_count, cudaStream_t stream);
+
 // Eviction (paged_evict.cu).
 struct EvictArgs {
     PagedBatch s;              // cu_q unused

@@ -1,0 +1,511 @@
+// paged_weights_tc.cu -- the attention weight that every cached key receives
+// from the rows of one call, bf16 on the tensor cores (definition and order as
+// in paged_weights.cu).
+//
+// S^T = K Q^T puts the keys on TMEM lanes, so a thread owns one key and adds up
+// its columns exp2(c s - lse log2 e) in a register: no maximum, no exchange.
+// The rows that see a key are those from its own token on, so the mask is one
+// first column per key.
+//
+// Work.  An item is 256 keys (two key tiles) of one key/value head; its units
+// are the query tiles (tt tokens, tt * G <= 128 rows) from the first token that
+// sees the item's first key.  As in paged_tc.cu every CTA of one launch takes
+// an equal share of all units and finds it itself.  With `split` a share may
+// begin and end inside an item, whose sums then go to the CTA's first or second
+// workspace slot, to be added in order by weights_merge_kernel; without it (one
+// query tile per item: decode) a CTA takes the items that begin in its share.
+//
+// Roles (320 threads): warp 0 TMA producer (K pair per item, Q tile and its
+// rows' lse per unit), warp 1 MMA issuer, warps 2-5 and 6-9 the two key tiles.
+// TMEM: two score buffers of 128 columns per key tile.
+//
+// Bound: decode reads K once (HBM); with many rows one exponential per score
+// binds (16 per clock and SM), the tensor cores need half that time.
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "kernels.h"
+#include "paged.cuh"
+#include "ptx.cuh"
+
+namespace mea {
+namespace {
+
+constexpr int kTile = 128;
+constexpr int kThreads = 320;
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <int D>
+struct Cfg {
+    static constexpr int kTileBytes = kTile * D * 2;
+    static constexpr int kBoxBytes = 128 * 128;
+    static constexpr int kPairs = 2;                          // K pairs in flight
+    static constexpr int kQStages = D == 128 ? 2 : 4;
+    static constexpr int kSmemData = (2 * kPairs + kQStages) * kTileBytes;
+    static constexpr int kLseBytes = kQStages * kTile * 4;
+    static constexpr int kSmemBytes = kSmemData + kLseBytes + 1024 /*barriers*/ + 1024 /*alignment slack*/;
+    static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+};
+
+struct Barriers {
+    uint64_t k_full[2], k_empty[2];
+    uint64_t q_full[4], q_empty[4];
+    uint64_t s_full[2][2], s_free[2][2];   // [key tile][buffer]
+    uint64_t drain;
+    unsigned tmem_base;
+    int abort_flag;
+    int b0, h0, i0, u0;
+    long long units;
+    long long warp_sum[kThreads / 32];
+};
+
+__device__ __forceinline__ int q_tiles(const Seq& sq, int tt) { return (sq.n + tt - 1) / tt; }
+__device__ __forceinline__ int items_of(const Seq& sq) { return sq.n > 0 ? (sq.L + 2 * kTile - 1) / (2 * kTile) : 0; }
+// first query tile of item i: the one of the first token that sees key 256 i
+__device__ __forceinline__ int first_tile(const Seq& sq, int tt, int i) {
+    return max(0, i * 2 * kTile - (sq.L - sq.n)) / tt;
+}
+__device__ __forceinline__ int units_of(const Seq& sq, int tt, int i) { return q_tiles(sq, tt) - first_tile(sq, tt, i); }
+// items that every query tile sees
+__device__ __forceinline__ int full_items(const Seq& sq) {
+    return sq.L < sq.n ? 0 : min(items_of(sq), (sq.L - sq.n) / (2 * kTile) + 1);
+}
+
+struct Walk {
+    Seq sq;
+    int b, h, i, items;
+    int u0, u1, n_units;
+    long long left;
+    bool first, split;
+
+    __device__ __forceinline__ void begin(const PagedWeightsTcArgs& a, const Barriers* bars) {
+        b = bars->b0;
+        h = bars->h0;
+        i = bars->i0;
+        u0 = bars->u0;
+        left = bars->units;
+        first = true;
+        split = a.split;
+        if (left <= 0) return;
+        sq = load_seq(a.s, b);
+        items = items_of(sq);
+        n_units = units_of(sq, a.tt, i);
+        u1 = split ? (int)min((long long)n_units, u0 + left) : n_units;
+        if (!split && u0 > 0) next(a);   // the item belongs to the CTA in front
+    }
+    __device__ __forceinline__ bool done() const { return left <= 0; }
+    __device__ __forceinline__ void next(const PagedWeightsTcArgs& a) {
+        left -= u1 - u0;
+        first = false;
+        if (left <= 0) return;
+        if (++i == items) {
+            i = 0;
+            if (++h == a.Hkv) {
+                h = 0;
+                do {
+                    ++b;
+                    if (b >= a.s.B) {
+                        left = 0;
+                        return;
+                    }
+                    sq = load_seq(a.s, b);
+                    items = items_of(sq);
+                } while (items == 0);
+            }
+        }
+        n_units = units_of(sq, a.tt, i);
+        u0 = 0;
+        u1 = split ? (int)min((long long)n_units, left) : n_units;
+    }
+    __device__ __forceinline__ bool whole() const { return u0 == 0 && u1 == n_units; }
+    __device__ __forceinline__ bool two() const { return i * 2 * kTile + kTile < sq.L; }   // the second key tile has keys
+};
+
+__device__ __forceinline__ void find_share(const PagedWeightsTcArgs& a, Barriers* bars) {
+    const int tid = (int)threadIdx.x;
+    const unsigned lane = lane_id(), warp = warp_id();
+    auto of_seq = [&](int b) {
+        const Seq sq = load_seq(a.s, b);
+        const int items = items_of(sq), full = full_items(sq);
+        long long sum = (long long)full * q_tiles(sq, a.tt);
+        for (int i = full; i < items; ++i) sum += units_of(sq, a.tt, i);
+        return sum * a.Hkv;
+    };
+    auto scan = [&](long long x, long long* all) {
+        long long upto = x;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= (unsigned)o) upto += y;
+        }
+        if (lane == 31) bars->warp_sum[warp] = upto;
+        __syncthreads();
+        long long before = 0, total = 0;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < (int)warp) before += bars->warp_sum[w];
+            total += bars->warp_sum[w];
+        }
+        __syncthreads();
+        *all = total;
+        return before + upto - x;
+    };
+    long long W = 0, mine = 0, block_before = 0;
+    for (int b0 = 0; b0 < a.s.B; b0 += kThreads) {
+        const int b = b0 + tid;
+        long long all;
+        mine = b < a.s.B ? of_seq(b) : 0;
+        block_before = scan(mine, &all);
+        W += all;
+    }
+    const long long c = blockIdx.x, C = gridDim.x;
+    const long long w0 = W * c / C, w1 = W * (c + 1) / C;
+    if (tid == 0) bars->units = w1 - w0;
+    auto locate = [&](int b, long long before, long long sum) {
+        if (w0 < before || w0 >= before + sum || w1 <= w0) return;
+        const Seq sq = load_seq(a.s, b);
+        const int items = items_of(sq), full = full_items(sq), nq = q_tiles(sq, a.tt);
+        const long long per_head = sum / a.Hkv;
+        long long x = w0 - before;
+        bars->b0 = b;
+        bars->h0 = (int)(x / per_head);
+        x -= bars->h0 * per_head;
+        int i = (int)min((long long)full, x / nq);
+        x -= (long long)i * nq;
+        for (; i >= full && i + 1 < items; ++i) {
+            const int n = units_of(sq, a.tt, i);
+            if (x < n) break;
+            x -= n;
+        }
+        bars->i0 = i;
+        bars->u0 = (int)x;
+    };
+    if (a.s.B <= kThreads) {
+        if (tid < a.s.B) locate(tid, block_before, mine);
+    } else {
+        long long base = 0;
+        for (int b0 = 0; b0 < a.s.B; b0 += kThreads) {
+            const int b = b0 + tid;
+            long long all;
+            const long long x = b < a.s.B ? of_seq(b) : 0;
+            const long long before = base + scan(x, &all);
+            if (b < a.s.B) locate(b, before, x);
+            base += all;
+        }
+    }
+    __syncthreads();
+}
+
+// Slot of key `key` of (b, h) in weights.
+__device__ __forceinline__ size_t weight_at(const PagedBatch& s, int Hkv, int b, int h, int key) {
+    return (((size_t)load_page(s, b, key >> s.page_shift) * Hkv + h) << s.page_shift) + (key & ((1 << s.page_shift) - 1));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                        const PagedWeightsTcArgs a) {
+    using C = Cfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint8_t* sK = smem;                                       // [pair][key tile]
+    uint8_t* sQ = smem + 2 * C::kPairs * C::kTileBytes;
+    float* sLse = reinterpret_cast<float*>(smem + C::kSmemData);   // [Q stage][row], times log2 e
+    Barriers* bars = reinterpret_cast<Barriers*>(smem + C::kSmemData + C::kLseBytes);
+    const unsigned warp = warp_id();
+    const unsigned lane = lane_id();
+    const int tt = a.tt;
+    const int G = a.H / a.Hkv;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars->k_full[i], 1);
+            mbar_init(&bars->k_empty[i], 1);
+            for (int j = 0; j < 2; ++j) {
+                mbar_init(&bars->s_full[i][j], 1);
+                mbar_init(&bars->s_free[i][j], 128);
+            }
+        }
+        for (int i = 0; i < C::kQStages; ++i) {
+            mbar_init(&bars->q_full[i], 2);    // the copies, and the rows' lse
+            mbar_init(&bars->q_empty[i], 257);   // both MMAs, and the readers of lse
+        }
+        mbar_init(&bars->drain, 1);
+        bars->abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(&bars->tmem_base, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const unsigned tmem = bars->tmem_base;
+    volatile int* abort_flag = &bars->abort_flag;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    find_share(a, bars);
+
+    Walk w;
+    w.begin(a, bars);
+    if (warp == 0) {
+        // ------------------------------------------------ producer
+        if (lane == 0) {
+            prefetch_tmap(&tm_q);
+            prefetch_tmap(&tm_k);
+            if (a.split) {
+                a.parts[2 * blockIdx.x].n_kv = 0;
+                a.parts[2 * blockIdx.x + 1].n_kv = 0;
+            }
+        }
+        const int shift = a.s.page_shift;
+        const int box_rows = min(kTile, 1 << shift);
+        constexpr int kHalves = D / 64;
+        const int boxes = kTile / box_rows * kHalves;
+        const int my_row = (int)lane / kHalves * box_rows;
+        const int my_half = (int)lane % kHalves;
+        const bool mine = (int)lane < boxes;
+        const int outside = a.s.num_pages * a.Hkv;
+        int li = 0, qc = 0;         // items and Q tiles asked for
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, unsigned parity) -> bool {
+            const int got = lane != 0 || mbar_wait(bar, parity, abort_flag);
+            return __shfl_sync(0xffffffffu, got, 0) != 0;
+        };
+        for (; ok && !w.done(); w.next(a)) {
+            const int ks = li & 1;
+            const int n_kt = w.two() ? 2 : 1;
+            if (li >= 2 && !(ok = wait(&bars->k_empty[ks], ((li >> 1) - 1) & 1))) break;
+            if (lane == 0) {
+                if (!w.whole()) {
+                    PagedPart& p = a.parts[2 * blockIdx.x + (w.first ? 0 : 1)];
+                    p.b = w.b;
+                    p.h = w.h;
+                    p.i = w.i;
+                    p.t0 = w.u0;
+                    p.t1 = w.u1;
+                    p.n_kv = w.n_units;
+                }
+                mbar_arrive_expect_tx(&bars->k_full[ks], (unsigned)(n_kt * C::kTileBytes));
+            }
+            __syncwarp();
+            for (int t = 0; t < n_kt; ++t) {
+                const int key = (2 * w.i + t) * kTile + my_row;
+                int z = outside;
+                if (mine && key < w.sq.L) z = load_page(a.s, w.b, key >> shift) * a.Hkv + w.h;
+                if (mine)
+                    tma_load_3d(sK + (2 * ks + t) * C::kTileBytes + my_half * C::kBoxBytes + my_row * 128, &tm_k,
+                                &bars->k_full[ks], my_half * 64, key & ((1 << shift) - 1), z);
+            }
+            ++li;
+            const int f = first_tile(w.sq, tt, w.i);
+            for (int u = w.u0; ok && u < w.u1; ++u) {
+                const int s = qc % C::kQStages;
+                const int tok0 = (f + u) * tt;
+                // the rows' lse, loaded while the stage drains
+                float ls[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int row = 32 * e + (int)lane;
+                    const int tok = tok0 + row / G;
+                    ls[e] = row < tt * G && tok < w.sq.n
+                                ? a.lse[(size_t)(w.sq.q0 + tok) * a.H + w.h * G + row % G] * kLog2e : 0.f;
+                }
+                if (qc >= C::kQStages && !(ok = wait(&bars->q_empty[s], (qc / C::kQStages - 1) & 1))) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&bars->q_full[s], (unsigned)(G * tt * D * 2));
+                    for (int x = 0; x < kHalves; ++x)
+                        tma_load_3d(sQ + s * C::kTileBytes + x * C::kBoxBytes, &tm_q, &bars->q_full[s], x * 64, w.h * G,
+                                    w.sq.q0 + tok0);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sLse[s * kTile + 32 * e + (int)lane] = ls[e];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->q_full[s]);
+                ++qc;
+            }
+        }
+        // never leave with copies in flight
+        for (int i = li > 2 ? li - 2 : 0; i < li; ++i) mbar_wait(&bars->k_full[i & 1], (i >> 1) & 1, nullptr);
+        for (int c = qc > C::kQStages ? qc - C::kQStages : 0; c < qc; ++c)
+            mbar_wait(&bars->q_full[c % C::kQStages], (c / C::kQStages) & 1, nullptr);
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            const unsigned idesc = make_idesc_bf16(128, (unsigned)((tt * G + 15) / 16 * 16), 0, 0);
+            const uint32_t k_lo = desc_lo_kmajor(smem_u32(sK));
+            const uint32_t q_lo = desc_lo_kmajor(smem_u32(sQ));
+            constexpr uint32_t kStep = C::kTileBytes >> 4;
+            bool ok = true;
+            int li = 0, qc = 0;
+            int cnt0 = 0, cnt1 = 0;   // units of each key tile: buffer and phase of s_full / s_free
+            for (; ok && !w.done(); w.next(a), ++li) {
+                const int ks = li & 1;
+                const bool two = w.two();
+                if (!(ok = mbar_wait(&bars->k_full[ks], (li >> 1) & 1, abort_flag))) break;
+                for (int u = w.u0; ok && u < w.u1; ++u, ++qc) {
+                    const int s = qc % C::kQStages;
+                    if (!(ok = mbar_wait(&bars->q_full[s], (qc / C::kQStages) & 1, abort_flag))) break;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        if (t == 1 && !two) break;
+                        const int cnt = t ? cnt1 : cnt0;
+                        const int buf = cnt & 1;
+                        if (cnt >= 2 && !(ok = mbar_wait(&bars->s_free[t][buf], ((cnt >> 1) - 1) & 1, abort_flag))) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk)
+                            mma_ss_lo(tmem + (unsigned)(t * 256 + buf * 128), k_lo + (2 * ks + t) * kStep + kmajor_step(kk),
+                                      q_lo + s * kStep + kmajor_step(kk), idesc, kk > 0);
+                        mma_commit(&bars->s_full[t][buf]);
+                        if (t) ++cnt1; else ++cnt0;
+                    }
+                    if (!ok) break;
+                    mma_commit(&bars->q_empty[s]);
+                }
+                if (ok) mma_commit(&bars->k_empty[ks]);
+            }
+            mma_commit(&bars->drain);
+            mbar_wait(&bars->drain, 0, nullptr);
+        }
+    } else {
+        // ------------------------------------------------ one thread per key
+        const int t = (warp - 2) >> 2;
+        const unsigned sub = warp & 3;
+        const int r = (int)sub * 32 + (int)lane;
+        const unsigned tS = tmem + ((sub * 32u) << 16) + (unsigned)t * 256u;
+        const float c_log2 = a.scale * kLog2e;
+        bool ok = true;
+        int cnt = 0, qc = 0;
+        for (; ok && !w.done(); w.next(a)) {
+            const int key = (2 * w.i + t) * kTile + r;
+            const bool work = t == 0 || w.two();
+            const bool mine = key < w.sq.L;
+            const bool whole = w.whole();
+            // the slot and its sum so far, loaded while the tiles arrive
+            size_t at = 0;
+            float old = 0.f;
+            if (mine && whole) {
+                at = weight_at(a.s, a.Hkv, w.b, w.h, key);
+                old = a.weights[at];
+            }
+            const int f = first_tile(w.sq, tt, w.i);
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int u = w.u0; u < w.u1; ++u, ++qc) {
+                const int s = qc % C::kQStages;
+                if (!(ok = mbar_wait(&bars->q_full[s], (qc / C::kQStages) & 1, abort_flag))) break;
+                if (!work) {
+                    mbar_arrive(&bars->q_empty[s]);
+                    continue;
+                }
+                const int buf = cnt & 1;
+                if (!(ok = mbar_wait(&bars->s_full[t][buf], (cnt >> 1) & 1, abort_flag))) break;
+                ++cnt;
+                tc_fence_after();
+                const int tok0 = (f + u) * tt;
+                const int rows = min(tt, w.sq.n - tok0) * G;
+                // the first column that sees this key, and whether some lane of the warp masks any
+                const int first = max(0, key - (w.sq.L - w.sq.n) - tok0) * G;
+                const bool masked = (key - (int)lane + 31 - (w.sq.L - w.sq.n) - tok0) > 0;
+                const float* ls = sLse + s * kTile;
+#pragma unroll
+                for (int c0 = 0; c0 < kTile; c0 += 32) {
+                    if (c0 >= rows) break;
+                    uint32_t x[32];
+                    tmem_ld32(tS + buf * 128 + c0, x);
+                    tmem_wait_ld();
+                    if (!masked && c0 + 32 <= rows) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4) {
+                            const float4 l4 = *reinterpret_cast<const float4*>(ls + c0 + i);
+                            sum[0] += ex2_approx(fmaf(__uint_as_float(x[i]), c_log2, -l4.x));
+                            sum[1] += ex2_approx(fmaf(__uint_as_float(x[i + 1]), c_log2, -l4.y));
+                            sum[2] += ex2_approx(fmaf(__uint_as_float(x[i + 2]), c_log2, -l4.z));
+                            sum[3] += ex2_approx(fmaf(__uint_as_float(x[i + 3]), c_log2, -l4.w));
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const float p = ex2_approx(fmaf(__uint_as_float(x[i]), c_log2, -ls[c0 + i]));
+                            if (c0 + i >= first && c0 + i < rows) sum[i & 3] += p;
+                        }
+                    }
+                }
+                tc_fence_before();
+                mbar_arrive(&bars->s_free[t][buf]);
+                mbar_arrive(&bars->q_empty[s]);
+            }
+            if (!ok) break;
+            const float total = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            if (whole) {
+                if (mine) a.weights[at] = old + total;
+            } else {
+                a.part_sum[(size_t)(2 * blockIdx.x + (w.first ? 0 : 1)) * 2 * kTile + t * kTile + r] = total;
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// Adds the parts of the item that CTA blockIdx.x began and did not finish, in
+// the order of their rows; a thread per key.
+__global__ void __launch_bounds__(2 * kTile) weights_merge_kernel(const PagedWeightsTcArgs a, int ctas) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    int c = (int)blockIdx.x;
+    int slot = 2 * c;
+    PagedPart p = a.parts[slot];
+    if (p.n_kv == 0 || p.t0 != 0) p = a.parts[++slot];
+    if (p.n_kv == 0 || p.t0 != 0) return;
+    const Seq sq = load_seq(a.s, p.b);
+    const int key = p.i * 2 * kTile + (int)threadIdx.x;
+    float sum = a.part_sum[(size_t)slot * 2 * kTile + threadIdx.x];
+    PagedPart e = p;
+    while (e.t1 < p.n_kv && c + 1 < ctas) {
+        const PagedPart n = a.parts[2 * ++c];
+        if (n.n_kv == 0) continue;   // with fewer units than CTAs some have no share
+        e = n;
+        sum += a.part_sum[(size_t)2 * c * 2 * kTile + threadIdx.x];
+    }
+    if (key < sq.L) a.weights[weight_at(a.s, a.Hkv, p.b, p.h, key)] += sum;
+}
+
+template <int D>
+cudaError_t launch_d(const PagedWeightsTcArgs& a, int sm_count, cudaStream_t stream) {
+    using C = Cfg<D>;
+    auto kern = paged_weights_tc_kernel<D>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)sm_count);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = C::kSmemBytes;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if ((e = cudaLaunchKernelEx(&cfg, kern, a.tm_q, a.tm_k, a)) != cudaSuccess) return e;
+    if ((e = cudaGetLastError()) != cudaSuccess || !a.split) return e;
+    cfg.blockDim = dim3(2 * kTile);
+    cfg.dynamicSmemBytes = 0;
+    if ((e = cudaLaunchKernelEx(&cfg, weights_merge_kernel, a, sm_count)) != cudaSuccess) return e;
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged_weights_tc(const PagedWeightsTcArgs& a, int sm_count, cudaStream_t stream) {
+    return a.D == 64 ? launch_d<64>(a, sm_count, stream) : launch_d<128>(a, sm_count, stream);
+}
+
+}  // namespace mea

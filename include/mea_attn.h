@@ -510,16 +510,21 @@ mea_status_t mea_attn_paged(const void* q, const void* k_cache, const void* v_ca
 /*
  * weights_j += sum over the rows i of the call's query heads of the key's group
  * that see key j of exp(scale * q_i . k_j - lse_i), with lse [T, H] from
- * mea_attn_paged of the same call: what key j contributed.  Every sum has one
- * owner and a fixed order (no atomics): the same inputs give the same bits.
+ * mea_attn_paged of the same call: what key j contributed.  The sums have a
+ * fixed order (no atomics): the same inputs give the same bits.  workspace: as
+ * for mea_attn_paged, of mea_attn_paged_weights_workspace_size bytes.
  * Two sequences of a call must not share a page here (each would add to the
  * same sums).  Errors: MEA_ERR_INVALID_ARG, MEA_ERR_UNSUPPORTED,
- * MEA_ERR_MISALIGNED, MEA_ERR_CUDA.
+ * MEA_ERR_MISALIGNED, MEA_ERR_WORKSPACE, MEA_ERR_CUDA.
  */
+mea_status_t mea_attn_paged_weights_workspace_size(int T, int B, int H, int H_kv, int D, int max_q, int max_kv,
+                                                   mea_dtype_t dtype, size_t* bytes);
+
 mea_status_t mea_attn_paged_weights(const void* q, const float* lse, const void* k_cache, float* weights,
                                     const int* cu_q, const int* kv_len, const int* page_table, int T, int B, int H,
                                     int H_kv, int D, long long q_stride, int num_pages, int page_size, int max_pages,
-                                    int max_q, int max_kv, float scale, mea_dtype_t dtype, void* stream);
+                                    int max_q, int max_kv, float scale, mea_dtype_t dtype, void* workspace,
+                                    size_t workspace_bytes, void* stream);
 
 /*
  * Cuts every sequence with more than n_keep cached keys to n_keep: each

@@ -41,7 +41,7 @@ def attend(lib, q=A, kc=A, vc=A, o=A, lse=A, cu=A, kv=A, table=A, T=4, B=2, H=4,
 def weigh(lib, q=A, lse=A, kc=A, w=A, cu=A, kv=A, table=A, T=4, B=2, H=4, Hkv=2, D=64, qs=256, pages=8, page=16,
           maxp=4, max_q=2, max_kv=64, scale=0.125, dtype=BF16):
     return lib.mea_attn_paged_weights(q, lse, kc, w, cu, kv, table, T, B, H, Hkv, D, qs, pages, page, maxp, max_q,
-                                      max_kv, scale, dtype, None)
+                                      max_kv, scale, dtype, None, 0, None)
 
 
 def evict(lib, kc=A, vc=A, w=A, table=A, kv=A, dst=A + 64, out=A, idx=A, B=2, Hkv=2, D=64, pages=8, page=16, maxp=4,
@@ -116,7 +116,11 @@ def test_evict_refusals(lib, status, args):
 
 def test_workspace_size_refusals(lib):
     out = ctypes.c_size_t(7)
-    f = lib.mea_attn_paged_workspace_size
+    check_sizes(lib.mea_attn_paged_workspace_size, out)
+    check_sizes(lib.mea_attn_paged_weights_workspace_size, out)
+
+
+def check_sizes(f, out):
     assert f(4, 2, 4, 2, 64, 2, 64, BF16, None) == INVALID
     assert f(4, 2, 5, 2, 64, 2, 64, BF16, ctypes.byref(out)) == INVALID
     assert f(4, 2, 4, 2, 96, 2, 64, BF16, ctypes.byref(out)) == UNSUPPORTED

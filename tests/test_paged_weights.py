@@ -33,8 +33,10 @@ def check(bt, lse, got):
 
 def run(bt, lse, q=None, max_q=None, max_kv=None):
     kc, w, cu, kv, tab = bt.gpu("k_cache", "weights", "cu", "kv_len", "table")
-    m.mea_attn_paged_weights(bt.q.cuda() if q is None else q, lse.cuda(), kc, w, cu, kv, tab,
-                             bt.max_q if max_q is None else max_q, bt.max_kv if max_kv is None else max_kv, bt.scale)
+    mq, mk = bt.max_q if max_q is None else max_q, bt.max_kv if max_kv is None else max_kv
+    n = m.mea_attn_paged_weights_workspace_size(bt.T, len(bt.lens), bt.H, bt.Hkv, bt.D, mq, mk, bt.dtype)
+    ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda") if n else None    # garbage: NaN
+    m.mea_attn_paged_weights(bt.q.cuda() if q is None else q, lse.cuda(), kc, w, cu, kv, tab, mq, mk, bt.scale, ws)
     return w
 
 
