@@ -54,15 +54,23 @@ constexpr float kRescaleThreshold = 8.0f;
 constexpr float kNoKey = -1e30f;  // reference maximum of a row that has seen no key (finite: no inf - inf)
 constexpr unsigned kIdescNegateA = 1u << 13;
 
-template <int D>
+// FEW: at most kFewRows rows per query tile (decode).  Their Q takes 2 KB per 64
+// head dims instead of 16 KB (the MMA's other rows read whatever follows, and a
+// row of S depends on its own row of Q alone), and the space goes to the ring:
+// six tiles in flight instead of four.
+constexpr int kFewRows = 16;
+
+template <int D, bool FEW>
 struct Cfg {
-    static constexpr int kQBytes = kTile * D * 2;
+    static constexpr int kQBox = FEW ? kFewRows * 128 : 128 * 128;   // 64 head dims of a query tile
+    static constexpr int kQBytes = D / 64 * kQBox;
     static constexpr int kTileBytes = kTile * D * 2;     // K or V tile
-    static constexpr int kStages = D == 128 ? 4 : 6;
+    static constexpr int kStages = D == 64 ? (FEW ? 8 : 6) : (FEW ? 6 : 4);
     static constexpr int kBoxBytes = 128 * 128;
-    static constexpr int kSmemData = 2 * kQBytes + kStages * kTileBytes;
+    static constexpr int kSmemData = (2 * kQBytes + kStages * kTileBytes + 1023) / 1024 * 1024;
     static constexpr int kMergeBytes = 2 * kTile * 2 * 4;   // both slots' (m, l) per row
-    static constexpr int kSmemBytes = kSmemData + kMergeBytes + 1024 /*barriers*/ + 1024 /*alignment slack*/;
+    static constexpr int kStageBytes = 8 * 2048;            // epilogue: 32 rows x 64 bytes per warp
+    static constexpr int kSmemBytes = kSmemData + kMergeBytes + kStageBytes + 2048 /*barriers, walks*/ + 1024 /*alignment*/;
     static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
 
@@ -73,9 +81,10 @@ struct Barriers {
     uint64_t o_final, merge_ready, drain;
     unsigned tmem_base;
     int abort_flag;
-    // this CTA's share: where it begins, and its key tiles
+    // this CTA's share: where it begins, and what it costs
+    Seq sq0;
     int b0, h0, i0, t0;
-    long long tiles;
+    long long cost;
     long long warp_sum[kThreads / 32];
 };
 
@@ -89,31 +98,35 @@ __device__ __forceinline__ int tiles_of(const Seq& sq, int tt, int i) {
     return max(1, (keys_seen(sq, (i + 1) * 2 * tt) + kTile - 1) / kTile);
 }
 
-// Position in the list of items; walks on item by item.
+// Position in the list of items; walks on item by item.  A key tile costs 1, and
+// so does an item's end (its epilogue takes about as long as a key tile).
 struct Walk {
     Seq sq;
     int b, h, i, items;
     int t0, t1, n_kv;       // key tiles [t0, t1) of the item's n_kv
-    long long left;         // tiles of the share from t0 on
+    long long left;         // of the share, from t0 on
     bool first;
 
-    __device__ __forceinline__ void begin(const PagedBatch& s, const Barriers* bars, int tt) {
+    __device__ __forceinline__ void begin(const PagedBatch& s, const Barriers* bars, int Hkv, int tt) {
+        sq = bars->sq0;
         b = bars->b0;
         h = bars->h0;
         i = bars->i0;
         t0 = bars->t0;
-        left = bars->tiles;
+        left = bars->cost;
         first = true;
-        if (left > 0) {
-            sq = load_seq(s, b);
-            items = items_of(sq, tt);
-            n_kv = tiles_of(sq, tt, i);
-            t1 = (int)min((long long)n_kv, t0 + left);
+        if (left <= 0) return;
+        items = items_of(sq, tt);
+        n_kv = tiles_of(sq, tt, i);
+        t1 = (int)min((long long)n_kv, t0 + left);
+        if (t0 == n_kv) {   // nothing but the end of an item, which the CTA in front has taken
+            next(s, Hkv, tt);
+            first = true;
         }
     }
     __device__ __forceinline__ bool done() const { return left <= 0; }
     __device__ __forceinline__ void next(const PagedBatch& s, int Hkv, int tt) {
-        left -= t1 - t0;
+        left -= n_kv + 1 - t0;
         first = false;
         if (left <= 0) return;
         if (++i == items) {
@@ -144,15 +157,16 @@ struct Walk {
     }
 };
 
-// Every thread of the CTA: the share [W c / C, W (c + 1) / C) of all key tiles.
+// Every thread of the CTA: the share [W c / C, W (c + 1) / C) of the cost of all items.
 __device__ __forceinline__ void find_share(const PagedTcArgs& a, Barriers* bars) {
     const int tid = (int)threadIdx.x;
     const unsigned lane = lane_id(), warp = warp_id();
+    Seq sq;
     auto of_seq = [&](int b) {
-        const Seq sq = load_seq(a.s, b);
+        sq = load_seq(a.s, b);
         const int items = items_of(sq, a.tt);
         long long sum = 0;
-        for (int i = 0; i < items; ++i) sum += tiles_of(sq, a.tt, i);
+        for (int i = 0; i < items; ++i) sum += tiles_of(sq, a.tt, i) + 1;
         return sum * a.Hkv;
     };
     // inclusive scan over the block's threads; returns the sum in front of this thread, *all the block's
@@ -185,19 +199,19 @@ __device__ __forceinline__ void find_share(const PagedTcArgs& a, Barriers* bars)
     }
     const long long c = blockIdx.x, C = gridDim.x;
     const long long w0 = W * c / C, w1 = W * (c + 1) / C;
-    if (tid == 0) bars->tiles = w1 - w0;
+    if (tid == 0) bars->cost = w1 - w0;
     auto locate = [&](int b, long long before, long long sum) {
         if (w0 < before || w0 >= before + sum || w1 <= w0) return;
-        const Seq sq = load_seq(a.s, b);
-        const int items = items_of(sq, a.tt);
+        const int items = items_of(sq, a.tt);   // sq is b's since of_seq(b)
         const long long per_head = sum / a.Hkv;
         long long x = w0 - before;
+        bars->sq0 = sq;
         bars->b0 = b;
         bars->h0 = (int)(x / per_head);
         x -= bars->h0 * per_head;
         int i = 0;
         for (; i + 1 < items; ++i) {
-            const int n = tiles_of(sq, a.tt, i);
+            const int n = tiles_of(sq, a.tt, i) + 1;
             if (x < n) break;
             x -= n;
         }
@@ -220,17 +234,19 @@ __device__ __forceinline__ void find_share(const PagedTcArgs& a, Barriers* bars)
     __syncthreads();
 }
 
-template <int D>
+template <int D, bool FEW>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ CUtensorMap tm_v, const PagedTcArgs a) {
-    using C = Cfg<D>;
+    using C = Cfg<D, FEW>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t* sQ = smem;
     uint8_t* sRing = smem + 2 * C::kQBytes;
     float* sMerge = reinterpret_cast<float*>(smem + C::kSmemData);
-    Barriers* bars = reinterpret_cast<Barriers*>(smem + C::kSmemData + C::kMergeBytes);
+    uint8_t* sStage = smem + C::kSmemData + C::kMergeBytes;
+    Barriers* bars = reinterpret_cast<Barriers*>(smem + C::kSmemData + C::kMergeBytes + C::kStageBytes);
+    static_assert(sizeof(Barriers) <= 1024 && 8 * sizeof(Walk) <= 1024, "shared memory");
 
     const unsigned warp = warp_id();
     const unsigned lane = lane_id();
@@ -271,10 +287,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     find_share(a, bars);
 
-    Walk w;
-    w.begin(a.s, bars, tt);
     if (warp == 0) {
         // ------------------------------------------------ TMA producer
+        Walk w;
+        w.begin(a.s, bars, a.Hkv, tt);
         if (lane == 0) {
             prefetch_tmap(&tm_q);
             prefetch_tmap(&tm_k);
@@ -314,7 +330,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 mbar_arrive_expect_tx(&bars->q_full, (unsigned)(n_qt * G * tt * D * 2));
                 for (int t = 0; t < n_qt; ++t)
                     for (int x = 0; x < kHalves; ++x)
-                        tma_load_3d(sQ + t * C::kQBytes + x * C::kBoxBytes, &tm_q, &bars->q_full, x * 64, w.h * G,
+                        tma_load_3d(sQ + t * C::kQBytes + x * C::kQBox, &tm_q, &bars->q_full, x * 64, w.h * G,
                                     w.sq.q0 + (2 * w.i + t) * tt);
             }
             q_asked = li + 1;
@@ -365,7 +381,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             auto issue_s = [&](unsigned tS, uint32_t q_lo, uint32_t k_off) {
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
-                    mma_ss_lo(tS, q_lo + kmajor_step(kk), ring_k_lo + k_off + kmajor_step(kk), idesc_s, kk > 0);
+                    mma_ss_lo(tS, q_lo + (kk >> 2) * (C::kQBox >> 4) + (kk & 3) * 2, ring_k_lo + k_off + kmajor_step(kk), idesc_s, kk > 0);
             };
             auto pv_halves = [&](int t, unsigned parity, uint32_t v_off, unsigned acc0) -> bool {
                 const unsigned tO = t ? tO1 : tO0, tS = t ? tS1 : tS0;
@@ -381,6 +397,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     mma_ts_lo(tO, tS + kk * 8, ring_v_lo + v_off + mnmajor_step(kk), idesc_o, 1u);
                 return true;
             };
+            Walk w;
+            w.begin(a.s, bars, a.Hkv, tt);
             bool ok = true, prev_single = false;
             int cnt0 = 0, cnt1 = 0;   // key tiles completed by each slot: phase of s_full / p_half / p_ready
             int li = 0;
@@ -492,12 +510,25 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         const int tok_r = r / G;               // token of row r in its query tile
         const int g_r = r - tok_r * G;
         const int page = 1 << a.s.page_shift;
+        // a wait that gives up does so for the whole warp: the code behind it is collective
+        auto wait_all = [&](uint64_t* bar, unsigned parity) -> bool {
+            return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
+        };
         bool ok = true;
         int kt = 0;         // key tiles completed by this slot (all items)
         int ring = 0;       // ring tiles in front of the current item
         int n_single = 0;   // single items completed by this CTA
         int li = 0;
-        for (; ok && !w.done(); w.next(a.s, a.Hkv, tt), ++li) {
+        // the warp's position lives in shared memory: the key tile loop needs the registers
+        Walk& w = reinterpret_cast<Walk*>(reinterpret_cast<uint8_t*>(bars) + 1024)[warp - 2];
+        if (lane == 0) w.begin(a.s, bars, a.Hkv, tt);
+        __syncwarp();
+        auto step = [&]() {
+            __syncwarp();
+            if (lane == 0) w.next(a.s, a.Hkv, tt);
+            __syncwarp();
+        };
+        for (; ok && !w.done(); step(), ++li) {
             const bool single = !w.two(tt);
             const int cnt = w.t1 - w.t0;
             const int n0 = single ? 0 : w.tiles_slot0(tt);
@@ -509,19 +540,25 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             const bool live = __any_sync(0xffffffffu, valid);   // rows of other lanes never meet this warp's
             // keys the row sees, from the item's first key tile on
             const int lim = max(0, w.sq.L - w.sq.n + min(tok0 + tok_r, w.sq.n - 1) + 1) - w.t0 * kTile;
-            const int len = w.sq.L - w.t0 * kTile;               // keys of the sequence, likewise
+            // from this key tile on some row of the warp is masked (uniform, so that
+            // the other tiles skip the selects by a branch)
+            const int mask_j = max(0, __reduce_min_sync(0xffffffffu, lim)) / kTile;
+            // The key tile (of this slot, else -1) whose values behind the
+            // sequence's last key are to be overwritten, and their first row.
+            const int last = (w.sq.L - 1) / kTile - w.t0;
+            const int nv = w.sq.L - (w.t0 + last) * kTile;
+            const int fix = w.sq.L > 0 && last < cnt && nv % page != 0 &&
+                            (single ? (last & 1) == t : t == (last < n0 ? 0 : 1)) ? last : -1;
             float m_ref = kNoKey;
             float l = 0.f;
             for (int it = 0; it < n_mine; ++it, ++kt) {
                 const int j = single ? 2 * it + t : it;          // key tile of this share of the item
-                if (!(ok = mbar_wait(&bars->s_full[t], kt & 1, abort_flag))) break;
+                if (!(ok = wait_all(&bars->s_full[t], kt & 1))) break;
                 tc_fence_after();
-                // values behind the sequence's last key: zeros, before any P V reads the tile
-                const int nv = len - j * kTile;
-                if (nv < kTile && nv > 0 && nv % page != 0 && (single || t == 0 || j >= n0)) {
+                if (j == fix) {   // zeros, before any P V reads the tile
                     const int c = ring + 2 * j + 1;
                     const int s = c % C::kStages;
-                    if (!(ok = mbar_wait(&bars->full[s], (c / C::kStages) & 1, abort_flag))) break;
+                    if (!(ok = wait_all(&bars->full[s], (c / C::kStages) & 1))) break;
                     const int stop = min(kTile, (nv + page - 1) / page * page);
                     uint8_t* tile = sRing + s * C::kTileBytes;
                     const int chunks = (stop - nv) * 8;           // 16-byte pieces of one box
@@ -541,8 +578,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
 #pragma unroll
                 for (int c0 = 0; c0 < kTile; c0 += 32) tmem_ld32(tS + c0, *reinterpret_cast<uint32_t(*)[32]>(&sr[c0]));
                 tmem_wait_ld();
-                const int nvalid = lim - j * kTile;
-                if (nvalid < kTile) {
+                if (j >= mask_j) {
+                    const int nvalid = lim - j * kTile;
 #pragma unroll
                     for (int c = 0; c < kTile; ++c)
                         if (c >= nvalid) sr[c] = __float_as_uint(-INFINITY);
@@ -616,11 +653,11 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             float w0 = 1.f, w1 = 0.f, M = m_ref, L = l;
             if (single) {
                 // the other slot has read the previous item's summaries
-                if (li > 0 && !(ok = mbar_wait(&bars->o_free[t ^ 1], (li - 1) & 1, abort_flag))) break;
+                if (li > 0 && !(ok = wait_all(&bars->o_free[t ^ 1], (li - 1) & 1))) break;
                 sMerge[2 * (t * kTile + r)] = m_ref;
                 sMerge[2 * (t * kTile + r) + 1] = l;
                 mbar_arrive(&bars->merge_ready);
-                if (!(ok = mbar_wait(&bars->merge_ready, n_single & 1, abort_flag))) break;
+                if (!(ok = wait_all(&bars->merge_ready, n_single & 1))) break;
                 ++n_single;
                 const float m_o = sMerge[2 * ((t ^ 1) * kTile + r)];
                 const float l_o = sMerge[2 * ((t ^ 1) * kTile + r) + 1];
@@ -630,61 +667,94 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 w0 = t ? w_oth : w_self;
                 w1 = t ? w_self : w_oth;
             }
-            if (!(ok = mbar_wait(&bars->o_final, li & 1, abort_flag))) break;
+            if (!(ok = wait_all(&bars->o_final, li & 1))) break;
             tc_fence_after();
-            if (live) {
-                const bool whole = w.whole();
-                const bool none = L == 0.f;     // no key in sight: O may never have been written
-                const float inv = none ? 0.f : whole ? 1.f / L : 1.f;
-                const float s0 = w0 * inv, s1 = w1 * inv;
-                const int c_begin = single ? t * (D / 2) : 0;
-                const int n_chunks = single ? D / 32 : D / 16;
-                const unsigned tOa = single ? tmem + lane_off + 256u : tO;
-                const unsigned tOb = tmem + lane_off + 384u;
-                const size_t orow = (size_t)(w.sq.q0 + tok0 + tok_r) * a.H + w.h * G + g_r;
-                const int prow = (2 * (int)blockIdx.x + (w.first ? 0 : 1)) * 2 * tt * G + (single ? 0 : t * tt * G) + r;
-                uint16_t* out = static_cast<uint16_t*>(a.o) + orow * D;
-                float* part = a.part_acc + (size_t)prow * D;
+            const bool whole = w.whole();
+            const bool none = L == 0.f;     // no key in sight: O may never have been written
+            const float inv = none ? 0.f : whole ? 1.f / L : 1.f;
+            const float s0 = w0 * inv, s1 = w1 * inv;
+            const int orow = (w.sq.q0 + tok0 + tok_r) * a.H + w.h * G + g_r;
+            const int prow = (2 * (int)blockIdx.x + (w.first ? 0 : 1)) * 2 * tt * G + (single ? 0 : t * tt * G) + r;
+            if (valid && (!single || t == 0)) {
+                if (whole)
+                    a.lse[orow] = none ? -INFINITY : (M + __log2f(L)) * kLn2;
+                else
+                    *reinterpret_cast<float2*>(a.part_ml + 2 * (size_t)prow) = make_float2(none ? -INFINITY : M, L);
+            }
+            // Rows go out through the warp's 2 KB of shared memory, 64 bytes of
+            // each of the 32 rows a round: a store instruction then covers 8 rows
+            // of 64 contiguous bytes, not 32 rows of 16.  16-byte pieces are
+            // permuted by row against bank conflicts.
+            uint8_t* stage = sStage + (warp - 2) * 2048;
+            const int dst = valid ? (whole ? orow : prow) : -1;
+            const int c_begin = single ? t * (D / 2) : 0;
+            auto put = [&](int q, const uint4& v) {   // piece q of this lane's row
+                *reinterpret_cast<uint4*>(stage + lane * 64 + ((q ^ ((lane >> 1) & 3)) * 16)) = v;
+            };
+            auto store = [&](void* base, size_t row_bytes, int byte0) {
+                __syncwarp();
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    if (k >= n_chunks) break;
-                    const int c0 = c_begin + 16 * k;
-                    uint32_t x[16];
-                    float f[16];
-                    tmem_ld16(tOa + c0, x);
-                    tmem_wait_ld();
+                for (int i = 0; i < 4; ++i) {
+                    const int rr = 8 * i + (int)lane / 4, q = (int)lane % 4;
+                    const int d = __shfl_sync(0xffffffffu, dst, rr);
+                    const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * 64 + ((q ^ ((rr >> 1) & 3)) * 16));
+                    if (d >= 0) *reinterpret_cast<uint4*>(static_cast<uint8_t*>(base) + d * row_bytes + byte0 + q * 16) = v;
+                }
+                __syncwarp();
+            };
+            // 64 accumulators at a time: of a two-tile item 64 columns of its own O,
+            // of a single item 32 columns of both O
+#pragma unroll 1
+            for (int pass = 0; live && pass < D / 64; ++pass) {
+                uint32_t x[2][32];
+                tmem_ld32(single ? tmem + lane_off + 256u + c_begin + 32 * pass : tO + 64 * pass, x[0]);
+                tmem_ld32(single ? tmem + lane_off + 384u + c_begin + 32 * pass : tO + 64 * pass + 32, x[1]);
+                tmem_wait_ld();
+                if (pass == D / 64 - 1) {   // the accumulators are free before the last rows are stored
+                    tc_fence_before();
+                    mbar_arrive(&bars->o_free[t]);
+                }
+                if (single) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) f[i] = none ? 0.f : __uint_as_float(x[i]) * s0;
-                    if (with1) {
-                        tmem_ld16(tOb + c0, x);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) f[i] = none ? 0.f : fmaf(__uint_as_float(x[i]), s1, f[i]);
+                    for (int c = 0; c < 32; ++c) {
+                        float f = __uint_as_float(x[0][c]) * s0;
+                        if (with1) f = fmaf(__uint_as_float(x[1][c]), s1, f);
+                        x[0][c] = __float_as_uint(none ? 0.f : f);
                     }
-                    if (!valid) continue;
-                    if (whole) {
-                        uint32_t packed[8];
+                } else {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) packed[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
-                        uint4* dst = reinterpret_cast<uint4*>(out + c0);
-                        dst[0] = make_uint4(packed[0], packed[1], packed[2], packed[3]);
-                        dst[1] = make_uint4(packed[4], packed[5], packed[6], packed[7]);
+                    for (int c = 0; c < 32; ++c) {
+                        x[0][c] = __float_as_uint(none ? 0.f : __uint_as_float(x[0][c]) * s0);
+                        x[1][c] = __float_as_uint(none ? 0.f : __uint_as_float(x[1][c]) * s0);
+                    }
+                }
+                const int col = single ? c_begin + 32 * pass : 64 * pass;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    if (k == 1 && single) break;
+                    if (whole) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            put(q, make_uint4(pack_bf16x2(__uint_as_float(x[k][8 * q]), __uint_as_float(x[k][8 * q + 1])),
+                                              pack_bf16x2(__uint_as_float(x[k][8 * q + 2]), __uint_as_float(x[k][8 * q + 3])),
+                                              pack_bf16x2(__uint_as_float(x[k][8 * q + 4]), __uint_as_float(x[k][8 * q + 5])),
+                                              pack_bf16x2(__uint_as_float(x[k][8 * q + 6]), __uint_as_float(x[k][8 * q + 7]))));
+                        store(a.o, D * 2, (col + 32 * k) * 2);
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 16; i += 4)
-                            *reinterpret_cast<float4*>(part + c0 + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+                        for (int c = 0; c < 32; c += 16) {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                put(q, make_uint4(x[k][c + 4 * q], x[k][c + 4 * q + 1], x[k][c + 4 * q + 2], x[k][c + 4 * q + 3]));
+                            store(a.part_acc, D * 4, (col + 32 * k + c) * 4);
+                        }
                     }
                 }
-                if (valid && (!single || t == 0)) {
-                    if (whole)
-                        a.lse[orow] = none ? -INFINITY : (M + __log2f(L)) * kLn2;
-                    else
-                        *reinterpret_cast<float2*>(a.part_ml + 2 * (size_t)prow) =
-                            make_float2(none ? -INFINITY : M, L);
-                }
             }
-            tc_fence_before();
-            mbar_arrive(&bars->o_free[t]);
+            if (!live) {
+                tc_fence_before();
+                mbar_arrive(&bars->o_free[t]);
+            }
         }
     }
 
@@ -698,48 +768,61 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
 
 // Joins the parts of the item that CTA blockIdx.x of the main kernel began and
 // did not finish: the first in one of its own slots, the others in the first
-// slots of the CTAs behind it.  grid.y: slices of the item's rows; a warp takes
-// a row, a lane D / 32 head dims.
+// slots of the CTAs behind it.  grid.y: slices of the item's rows.  W warps take
+// a row, each every W-th part, a lane D / 32 head dims; the warps' results are
+// joined through shared memory (W = 8 where an item has few rows: decode cuts a
+// long cache into many parts).
 constexpr int kMergeThreads = 256;
-constexpr int kMergeRows = 32;    // rows per CTA
 constexpr int kMergeBatch = 4;
 
-template <int DPL>
+template <int DPL, int W>
 __global__ void __launch_bounds__(kMergeThreads) paged_tc_merge_kernel(const PagedTcArgs a, int ctas) {
     constexpr int D = 32 * DPL;
+    constexpr int kRows = kMergeThreads / 32 / W;     // rows at a time
+    __shared__ float s_acc[W > 1 ? W : 1][D];
+    __shared__ float2 s_ml[W > 1 ? W : 1];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int c0 = (int)blockIdx.x;
+    const int warp = (int)warp_id(), lane = (int)lane_id();
     int slot = 2 * c0;
     PagedPart p = a.parts[slot];
     if (p.n_kv == 0 || p.t0 != 0) p = a.parts[++slot];
-    if (p.n_kv == 0 || p.t0 != 0) return;
-    int c1 = c0;                       // last CTA with a part
-    {
-        PagedPart e = p;
-        while (e.t1 < p.n_kv && c1 + 1 < ctas) {
-            const PagedPart n = a.parts[2 * ++c1];
-            if (n.n_kv != 0) e = n;   // with fewer tiles than CTAs some have no share
+    if (p.n_kv == 0 || p.t0 != 0 || p.t1 == p.n_kv) return;
+    // the CTA that holds the last part; with little work some CTAs between have none
+    int c1 = ctas - 1;
+    for (int c = c0 + 1; c < ctas; c += 32) {
+        bool end = false;
+        if (c + lane < ctas) {
+            const PagedPart n = a.parts[2 * (c + lane)];
+            end = n.n_kv != 0 && n.t1 == n.n_kv;
+        }
+        const unsigned ends = __ballot_sync(0xffffffffu, end);
+        if (ends) {
+            c1 = c + __ffs((int)ends) - 1;
+            break;
         }
     }
     const Seq sq = load_seq(a.s, p.b);
     const int G = a.H / a.Hkv;
     const int rows = 2 * a.tt * G;
-    const int warp = (int)warp_id(), lane = (int)lane_id();
-    for (int r = (int)blockIdx.y * kMergeRows + warp; r < min(rows, ((int)blockIdx.y + 1) * kMergeRows);
-         r += kMergeThreads / 32) {
+    const int per = (rows + (int)gridDim.y - 1) / (int)gridDim.y;
+    const int wi = warp % W;
+    for (int r0 = (int)blockIdx.y * per; r0 < min(rows, ((int)blockIdx.y + 1) * per); r0 += kRows) {
+        const int r = r0 + warp / W;
         const int tok = p.i * 2 * a.tt + r / G;
-        if (tok >= sq.n) break;
+        if (r >= min(rows, ((int)blockIdx.y + 1) * per) || tok >= sq.n) break;   // W > 1: the same for all warps
         float M = -INFINITY, L = 0.f, A[DPL];
 #pragma unroll
         for (int i = 0; i < DPL; ++i) A[i] = 0.f;
-        for (int c = c0; c <= c1; c += kMergeBatch) {
+        for (int c = c0 + wi; c <= c1; c += W * kMergeBatch) {
             float mc[kMergeBatch], lc[kMergeBatch], x[kMergeBatch][DPL];
 #pragma unroll
             for (int u = 0; u < kMergeBatch; ++u) {
+                const int cu = c + u * W;
                 mc[u] = -INFINITY;
-                if (c + u <= c1 && (c + u == c0 || a.parts[2 * (c + u)].n_kv != 0)) {
-                    const size_t row = (size_t)(c + u == c0 ? slot : 2 * (c + u)) * rows + r;
+                if (cu <= c1 && (cu == c0 || a.parts[2 * cu].n_kv != 0)) {
+                    const size_t row = (size_t)(cu == c0 ? slot : 2 * cu) * rows + r;
                     const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + 2 * row);
                     mc[u] = ml.x;
                     lc[u] = ml.y;
@@ -758,6 +841,28 @@ __global__ void __launch_bounds__(kMergeThreads) paged_tc_merge_kernel(const Pag
                 for (int i = 0; i < DPL; ++i) A[i] = fmaf(wc, x[u][i], A[i] * al);
             }
         }
+        if constexpr (W > 1) {
+            if (r0 > (int)blockIdx.y * per) __syncthreads();   // the last row's have been read
+#pragma unroll
+            for (int i = 0; i < DPL; ++i) s_acc[wi][lane * DPL + i] = A[i];
+            if (lane == 0) s_ml[wi] = make_float2(M, L);
+            __syncthreads();
+            if (wi != 0) continue;
+            M = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < W; ++k) M = fmaxf(M, s_ml[k].x);
+            L = 0.f;
+#pragma unroll
+            for (int i = 0; i < DPL; ++i) A[i] = 0.f;
+#pragma unroll
+            for (int k = 0; k < W; ++k) {
+                const float2 ml = s_ml[k];
+                const float wk = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
+                L = fmaf(wk, ml.y, L);
+#pragma unroll
+                for (int i = 0; i < DPL; ++i) A[i] = fmaf(wk, s_acc[k][lane * DPL + i], A[i]);
+            }
+        }
         const float inv = L == 0.f ? 0.f : 1.f / L;
         const size_t row = (size_t)(sq.q0 + tok) * a.H + p.h * G + r % G;
         uint16_t* out = static_cast<uint16_t*>(a.o) + row * D + lane * DPL;
@@ -768,10 +873,10 @@ __global__ void __launch_bounds__(kMergeThreads) paged_tc_merge_kernel(const Pag
     }
 }
 
-template <int D>
+template <int D, bool FEW>
 cudaError_t launch_d(const PagedTcArgs& a, int sm_count, cudaStream_t stream) {
-    using C = Cfg<D>;
-    auto kern = paged_tc_kernel<D>;
+    using C = Cfg<D, FEW>;
+    auto kern = paged_tc_kernel<D, FEW>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];
@@ -787,11 +892,11 @@ cudaError_t launch_d(const PagedTcArgs& a, int sm_count, cudaStream_t stream) {
     if ((e = cudaLaunchKernelEx(&cfg, kern, a.tm_q, a.tm_k, a.tm_v, a)) != cudaSuccess) return e;
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const int rows = 2 * a.tt * (a.H / a.Hkv);
-    cfg.gridDim = dim3((unsigned)sm_count, (unsigned)((rows + kMergeRows - 1) / kMergeRows));
+    cfg.gridDim = dim3((unsigned)sm_count, (unsigned)(FEW ? 1 : (rows + 31) / 32));
     cfg.blockDim = dim3(kMergeThreads);
     cfg.dynamicSmemBytes = 0;
-    if ((e = cudaLaunchKernelEx(&cfg, paged_tc_merge_kernel<D / 32>, a, sm_count)) != cudaSuccess) return e;
-    return cudaGetLastError();
+    e = cudaLaunchKernelEx(&cfg, paged_tc_merge_kernel<D / 32, FEW ? 8 : 1>, a, sm_count);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
@@ -803,7 +908,9 @@ int paged_tc_tokens(int G, int max_q) {
 }
 
 cudaError_t launch_paged_tc(const PagedTcArgs& a, int sm_count, cudaStream_t stream) {
-    return a.D == 64 ? launch_d<64>(a, sm_count, stream) : launch_d<128>(a, sm_count, stream);
+    const bool few = a.tt * (a.H / a.Hkv) <= kFewRows;
+    if (a.D == 64) return few ? launch_d<64, true>(a, sm_count, stream) : launch_d<64, false>(a, sm_count, stream);
+    return few ? launch_d<128, true>(a, sm_count, stream) : launch_d<128, false>(a, sm_count, stream);
 }
 
 }  // namespace mea
