@@ -16,8 +16,8 @@ mea_status_t api_fail(mea_status_t st, const char* where, const char* detail);
 mea_status_t api_cuda(cudaError_t e, const char* where);
 // The current device's SM count; MEA_ERR_UNSUPPORTED unless it is an sm_100.
 mea_status_t api_device(int* sm_count);
-// 3-D map, 128-byte swizzle, rows outside the tensor read as zero; elem_bytes 2 (bf16).
-mea_status_t api_map_bf16(CUtensorMap* m, const void* base, const cuuint64_t (&dims)[3],
-                          const cuuint64_t (&strides)[2], const cuuint32_t (&box)[3], const char* what);
+// bf16 map of `rank` dims, 128-byte swizzle, elements outside the tensor read as zero.
+mea_status_t api_map_bf16(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
+                          const cuuint64_t* strides, const cuuint32_t* box, const char* what);
 
 }  // namespace mea

@@ -112,13 +112,14 @@ mea_status_t map_q(CUtensorMap* m, const void* q, int T, int H, int G, int D, lo
     const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)T};
     const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)q_stride * 2};
     const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)tt};
-    return mea::api_map_bf16(m, q, dims, strides, box, "q");
+    return mea::api_map_bf16(m, q, 3, dims, strides, box, "q");
 }
 mea_status_t map_pages(CUtensorMap* m, const void* cache, int num_pages, int H_kv, int page_size, int D) {
-    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)page_size, (cuuint64_t)num_pages * H_kv};
-    const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)page_size * D * 2};
-    const cuuint32_t box[3] = {64, (cuuint32_t)std::min(page_size, 128), 1};
-    return mea::api_map_bf16(m, cache, dims, strides, box, "cache");
+    // {64 head dims, 8 keys, blocks of head dims, groups of 8 keys, (page, head)}: PageTile's layout
+    const cuuint64_t dims[5] = {64, 8, (cuuint64_t)D / 64, (cuuint64_t)page_size / 8, (cuuint64_t)num_pages * H_kv};
+    const cuuint64_t strides[4] = {(cuuint64_t)D * 2, 128, (cuuint64_t)D * 16, (cuuint64_t)page_size * D * 2};
+    const cuuint32_t box[5] = {64, 8, (cuuint32_t)D / 64, (cuuint32_t)std::min(page_size, 128) / 8, 1};
+    return mea::api_map_bf16(m, cache, 5, dims, strides, box, "cache");
 }
 
 struct WeightsPlan {

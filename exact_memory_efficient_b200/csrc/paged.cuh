@@ -43,6 +43,26 @@ __device__ __forceinline__ int load_page(const PagedBatch& s, int b, int i) {
     return 0;
 }
 
+// A tile of 128 keys of bf16 pages in shared memory, as one TMA box per page
+// lays it out: groups of 8 keys, in a group the blocks of 64 head dims, in a
+// block 8 rows of 128 bytes (128-byte swizzle).  Groups and blocks keep their
+// distances from page to page, so a tile of any page size is one operand with
+// the same descriptors; a box per page and block, with the blocks 16 KB apart,
+// takes twice the TMA instructions.
+template <int D>
+struct PageTile {
+    static constexpr int kGroupBytes = 8 * D * 2;
+    static constexpr int kBytes = 128 * D * 2;
+    static constexpr uint32_t kHi = desc_hi_sw128(kGroupBytes);
+    // K-major operand (K): step kk of 16 head dims, in 16-byte units
+    static constexpr uint32_t kmajor(int kk) { return (kk >> 2) * 64u + (kk & 3) * 2u; }
+    // MN-major operand (V): blocks of 64 head dims 1 KB apart; step kk of 16 keys
+    __device__ static uint32_t mn_lo(unsigned smem_addr) { return (smem_addr >> 4) | (64u << 16); }
+    static constexpr uint32_t mnmajor(int kk) { return kk * 2u * (kGroupBytes >> 4); }
+    // byte offset of key r, block x
+    __device__ static int row(int r, int x) { return (r >> 3) * kGroupBytes + x * 1024 + (r & 7) * 128; }
+};
+
 // Packed rows are cut into tiles of `per` rows that start anew with every
 // sequence.  Tile x belongs to the sequence b with start(b) <= x < start(b + 1),
 // where start(b) = floor(cu_q[b] * mul / per) + b: since

@@ -18,11 +18,15 @@
 // keys.  Every CTA finds its share by summing the key tiles of all sequences
 // itself; nothing is planned on the host, and a captured launch follows the
 // lengths that it finds.
+// (Cutting the list into several rounds of shares, so that the CTAs work on the
+// same heads at a time and their keys stay in L2, cost more in split items than it
+// gained: 4 prompts of 4096 tokens, 16 heads: 375 us in one round, 390 in two, 447
+// in four.)
 //
 // Roles and TMEM are those of fwd_persist.cu (320 threads):
 //   warp 0       TMEM allocator, then TMA producer: Q tiles per item, then K_0,
-//                V_0, K_1, V_1, ... of the item through the ring, one lane per
-//                (page, 64 head dims) box; no multicast.  Pages behind the
+//                V_0, K_1, V_1, ... of the item through the ring, one lane and box per
+//                page; no multicast.  Pages behind the
 //                sequence's last key are not looked up: their boxes lie outside
 //                the tensor and read as zero.
 //   warp 1       MMA issuer (one thread)
@@ -66,25 +70,44 @@ struct Cfg {
     static constexpr int kQBytes = D / 64 * kQBox;
     static constexpr int kTileBytes = kTile * D * 2;     // K or V tile
     static constexpr int kStages = D == 64 ? (FEW ? 8 : 6) : (FEW ? 6 : 4);
-    static constexpr int kBoxBytes = 128 * 128;
     static constexpr int kSmemData = (2 * kQBytes + kStages * kTileBytes + 1023) / 1024 * 1024;
     static constexpr int kMergeBytes = 2 * kTile * 2 * 4;   // both slots' (m, l) per row
     static constexpr int kStageBytes = 8 * 2048;            // epilogue: 32 rows x 64 bytes per warp
-    static constexpr int kSmemBytes = kSmemData + kMergeBytes + kStageBytes + 2048 /*barriers, walks*/ + 1024 /*alignment*/;
+    static constexpr int kSmemBytes = kSmemData + kMergeBytes + kStageBytes + 1024 /*barriers*/ + 1024 /*alignment*/;
     static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+};
+
+// An item as the softmax warps need it, written by the MMA issuer when it begins
+// the item.  Four of them: the issuer is at most two items ahead of a slot.
+struct Item {
+    int cnt;          // key tiles of the CTA's part; 0: no more items
+    int n0;           // of those, the ones that query tile 0 of a two-tile item sees
+    int single;       // one query tile: both slots on its rows
+    int tok0;         // first token
+    int n, q0;        // new tokens of the sequence, its first packed row
+    int seen;         // keys in front of the new tokens' own
+    int L;            // cached keys
+    int base;         // first key of the part
+    int h;
+    int part;         // the CTA's workspace slot for it, or -1: the item is whole
+    int pad;
 };
 
 struct Barriers {
     uint64_t q_full, q_empty;
     uint64_t full[8], empty[8];
-    uint64_t s_full[2], p_half[2], p_ready[2], o_free[2];
-    uint64_t o_final, merge_ready, drain;
+    uint64_t s_full[2], p_half[2], p_ready[2], o_free[2], o_final[2];
+    uint64_t item[4];
+    uint64_t merge_ready, drain;
+    Item items[4];
     unsigned tmem_base;
     int abort_flag;
     // this CTA's share: where it begins, and what it costs
-    Seq sq0;
-    int b0, h0, i0, t0;
-    long long cost;
+    struct Share {
+        Seq sq;
+        int b, h, i, t0;
+        long long cost;
+    } share;
     long long warp_sum[kThreads / 32];
 };
 
@@ -107,13 +130,13 @@ struct Walk {
     long long left;         // of the share, from t0 on
     bool first;
 
-    __device__ __forceinline__ void begin(const PagedBatch& s, const Barriers* bars, int Hkv, int tt) {
-        sq = bars->sq0;
-        b = bars->b0;
-        h = bars->h0;
-        i = bars->i0;
-        t0 = bars->t0;
-        left = bars->cost;
+    __device__ __forceinline__ void begin(const PagedBatch& s, const Barriers::Share& at, int Hkv, int tt) {
+        sq = at.sq;
+        b = at.b;
+        h = at.h;
+        i = at.i;
+        t0 = at.t0;
+        left = at.cost;
         first = true;
         if (left <= 0) return;
         items = items_of(sq, tt);
@@ -157,7 +180,7 @@ struct Walk {
     }
 };
 
-// Every thread of the CTA: the share [W c / C, W (c + 1) / C) of the cost of all items.
+// Every thread of the CTA: finds its share [W c / C, W (c + 1) / C) of the cost W of all items.
 __device__ __forceinline__ void find_share(const PagedTcArgs& a, Barriers* bars) {
     const int tid = (int)threadIdx.x;
     const unsigned lane = lane_id(), warp = warp_id();
@@ -197,26 +220,26 @@ __device__ __forceinline__ void find_share(const PagedTcArgs& a, Barriers* bars)
         block_before = scan(mine, &all);
         W += all;
     }
-    const long long c = blockIdx.x, C = gridDim.x;
-    const long long w0 = W * c / C, w1 = W * (c + 1) / C;
-    if (tid == 0) bars->cost = w1 - w0;
+    const long long w0 = W * blockIdx.x / gridDim.x, w1 = W * (blockIdx.x + 1) / gridDim.x;
+    if (tid == 0) bars->share.cost = w1 - w0;
     auto locate = [&](int b, long long before, long long sum) {
         if (w0 < before || w0 >= before + sum || w1 <= w0) return;
         const int items = items_of(sq, a.tt);   // sq is b's since of_seq(b)
         const long long per_head = sum / a.Hkv;
         long long x = w0 - before;
-        bars->sq0 = sq;
-        bars->b0 = b;
-        bars->h0 = (int)(x / per_head);
-        x -= bars->h0 * per_head;
+        Barriers::Share& at = bars->share;
+        at.sq = sq;
+        at.b = b;
+        at.h = (int)(x / per_head);
+        x -= at.h * per_head;
         int i = 0;
         for (; i + 1 < items; ++i) {
             const int n = tiles_of(sq, a.tt, i) + 1;
             if (x < n) break;
             x -= n;
         }
-        bars->i0 = i;
-        bars->t0 = (int)x;
+        at.i = i;
+        at.t0 = (int)x;
     };
     if (a.s.B <= kThreads) {
         if (tid < a.s.B) locate(tid, block_before, mine);
@@ -246,7 +269,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     float* sMerge = reinterpret_cast<float*>(smem + C::kSmemData);
     uint8_t* sStage = smem + C::kSmemData + C::kMergeBytes;
     Barriers* bars = reinterpret_cast<Barriers*>(smem + C::kSmemData + C::kMergeBytes + C::kStageBytes);
-    static_assert(sizeof(Barriers) <= 1024 && 8 * sizeof(Walk) <= 1024, "shared memory");
+    static_assert(sizeof(Barriers) <= 1024, "shared memory");
 
     const unsigned warp = warp_id();
     const unsigned lane = lane_id();
@@ -265,8 +288,9 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             mbar_init(&bars->p_half[t], 128);
             mbar_init(&bars->p_ready[t], 128);
             mbar_init(&bars->o_free[t], 128);
+            mbar_init(&bars->o_final[t], 1);
         }
-        mbar_init(&bars->o_final, 1);
+        for (int i = 0; i < 4; ++i) mbar_init(&bars->item[i], 1);
         mbar_init(&bars->merge_ready, 256);
         mbar_init(&bars->drain, 1);
         bars->abort_flag = 0;
@@ -275,6 +299,11 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     if (warp == 0) {
         tmem_alloc(&bars->tmem_base, 512);
         tmem_relinquish();
+        if (lane == 0) {   // kernel parameters: no need to wait for the kernel in front
+            prefetch_tmap(&tm_q);
+            prefetch_tmap(&tm_k);
+            prefetch_tmap(&tm_v);
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -290,21 +319,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     if (warp == 0) {
         // ------------------------------------------------ TMA producer
         Walk w;
-        w.begin(a.s, bars, a.Hkv, tt);
-        if (lane == 0) {
-            prefetch_tmap(&tm_q);
-            prefetch_tmap(&tm_k);
-            prefetch_tmap(&tm_v);
-            a.parts[2 * blockIdx.x].n_kv = 0;       // no part yet
-            a.parts[2 * blockIdx.x + 1].n_kv = 0;
-        }
         const int shift = a.s.page_shift;
         const int box_rows = min(kTile, 1 << shift);
-        constexpr int kHalves = D / 64;
-        const int boxes = kTile / box_rows * kHalves;    // of a tile: at most 16
-        const int my_row = (int)lane / kHalves * box_rows;   // lane's box: first key in the tile,
-        const int my_half = (int)lane % kHalves;              // 64 head dims
-        const bool mine = (int)lane < boxes;
+        const int my_row = (int)lane * box_rows;         // first key of the lane's box in the tile
+        const bool mine = my_row < kTile;
         const int outside = a.s.num_pages * a.Hkv;       // a page behind the tensor: reads as zero
         int c_glob = 0;
         int li = 0, q_asked = 0;    // items; those whose Q has been asked for
@@ -314,22 +332,26 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             const int got = lane != 0 || mbar_wait(bar, parity, abort_flag);
             return __shfl_sync(0xffffffffu, got, 0) != 0;
         };
-        for (; ok && !w.done(); w.next(a.s, a.Hkv, tt), ++li) {
+        const int slot = 2 * (int)blockIdx.x;           // the CTA's workspace slots
+        if (lane == 0) a.parts[slot].n_kv = a.parts[slot + 1].n_kv = 0;     // no part yet
+        for (w.begin(a.s, bars->share, a.Hkv, tt); ok && !w.done(); w.next(a.s, a.Hkv, tt), ++li) {
             const int n_qt = w.two(tt) ? 2 : 1;
             if (li > 0 && !(ok = wait(&bars->q_empty, (li - 1) & 1))) break;
             if (lane == 0) {
                 if (!w.whole()) {
-                    PagedPart& p = a.parts[2 * blockIdx.x + (w.first ? 0 : 1)];
+                    PagedPart& p = a.parts[slot + (w.first ? 0 : 1)];
                     p.b = w.b;
                     p.h = w.h;
                     p.i = w.i;
                     p.t0 = w.t0;
                     p.t1 = w.t1;
                     p.n_kv = w.n_kv;
+                    p.q0 = w.sq.q0;
+                    p.n = w.sq.n;
                 }
                 mbar_arrive_expect_tx(&bars->q_full, (unsigned)(n_qt * G * tt * D * 2));
                 for (int t = 0; t < n_qt; ++t)
-                    for (int x = 0; x < kHalves; ++x)
+                    for (int x = 0; x < D / 64; ++x)
                         tma_load_3d(sQ + t * C::kQBytes + x * C::kQBox, &tm_q, &bars->q_full, x * 64, w.h * G,
                                     w.sq.q0 + (2 * w.i + t) * tt);
             }
@@ -339,7 +361,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 const int key = j * kTile + my_row;
                 int z = outside;
                 if (mine && key < w.sq.L) z = load_page(a.s, w.b, key >> shift) * a.Hkv + w.h;
-                const int y = key & ((1 << shift) - 1);
+                const int group = (key & ((1 << shift) - 1)) >> 3;
 #pragma unroll
                 for (int v = 0; v < 2; ++v, ++c_glob) {
                     const int s = c_glob % C::kStages;
@@ -347,8 +369,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     if (lane == 0) mbar_arrive_expect_tx(&bars->full[s], C::kTileBytes);
                     __syncwarp();
                     if (mine)
-                        tma_load_3d(sRing + s * C::kTileBytes + my_half * C::kBoxBytes + my_row * 128,
-                                    v ? &tm_v : &tm_k, &bars->full[s], my_half * 64, y, z);
+                        tma_load_5d(sRing + s * C::kTileBytes + PageTile<D>::row(my_row, 0), v ? &tm_v : &tm_k,
+                                    &bars->full[s], 0, 0, 0, group, z);
                     __syncwarp();
                 }
             }
@@ -366,7 +388,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             const uint32_t q_lo0 = desc_lo_kmajor(smem_u32(sQ));
             const uint32_t q_lo1 = desc_lo_kmajor(smem_u32(sQ + C::kQBytes));
             const uint32_t ring_k_lo = desc_lo_kmajor(smem_u32(sRing));
-            const uint32_t ring_v_lo = desc_lo_mnmajor(smem_u32(sRing));
+            const uint32_t ring_v_lo = PageTile<D>::mn_lo(smem_u32(sRing));
             constexpr uint32_t kStageStep = C::kTileBytes >> 4;
             const unsigned tS0 = tmem, tS1 = tmem + 128u, tO0 = tmem + 256u, tO1 = tmem + 384u;
             int stage = 0;
@@ -381,7 +403,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             auto issue_s = [&](unsigned tS, uint32_t q_lo, uint32_t k_off) {
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
-                    mma_ss_lo(tS, q_lo + (kk >> 2) * (C::kQBox >> 4) + (kk & 3) * 2, ring_k_lo + k_off + kmajor_step(kk), idesc_s, kk > 0);
+                    mma_ss_desc(tS, q_lo + (kk >> 2) * (C::kQBox >> 4) + (kk & 3) * 2, kDescHiSw128,
+                                ring_k_lo + k_off + PageTile<D>::kmajor(kk), PageTile<D>::kHi, idesc_s, kk > 0);
             };
             auto pv_halves = [&](int t, unsigned parity, uint32_t v_off, unsigned acc0) -> bool {
                 const unsigned tO = t ? tO1 : tO0, tS = t ? tS1 : tS0;
@@ -389,22 +412,43 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < kTile / 32; ++kk)
-                    mma_ts_lo(tO, tS + kk * 8, ring_v_lo + v_off + mnmajor_step(kk), idesc_o, (acc0 | kk) ? 1u : 0u);
+                    mma_ts_desc(tO, tS + kk * 8, ring_v_lo + v_off + PageTile<D>::mnmajor(kk), PageTile<D>::kHi, idesc_o,
+                                (acc0 | kk) ? 1u : 0u);
                 if (!mbar_wait(&bars->p_ready[t], parity, abort_flag)) return false;
                 tc_fence_after();
 #pragma unroll
                 for (int kk = kTile / 32; kk < kTile / 16; ++kk)
-                    mma_ts_lo(tO, tS + kk * 8, ring_v_lo + v_off + mnmajor_step(kk), idesc_o, 1u);
+                    mma_ts_desc(tO, tS + kk * 8, ring_v_lo + v_off + PageTile<D>::mnmajor(kk), PageTile<D>::kHi, idesc_o, 1u);
                 return true;
             };
             Walk w;
-            w.begin(a.s, bars, a.Hkv, tt);
             bool ok = true, prev_single = false;
             int cnt0 = 0, cnt1 = 0;   // key tiles completed by each slot: phase of s_full / p_half / p_ready
             int li = 0;
-            for (; ok && !w.done(); w.next(a.s, a.Hkv, tt), ++li) {
+            for (w.begin(a.s, bars->share, a.Hkv, tt); ok && !w.done(); w.next(a.s, a.Hkv, tt), ++li) {
                 const bool single = !w.two(tt);
                 const int n1 = w.t1 - w.t0;
+                const int n0 = single ? 0 : w.tiles_slot0(tt);   // <= n1
+                {
+                    Item& it = bars->items[li & 3];
+                    it.cnt = n1;
+                    it.n0 = n0;
+                    it.single = single;
+                    it.tok0 = 2 * w.i * tt;
+                    it.n = w.sq.n;
+                    it.q0 = w.sq.q0;
+                    it.seen = w.sq.L - w.sq.n;
+                    it.L = w.sq.L;
+                    it.base = w.t0 * kTile;
+                    it.h = w.h;
+                    it.part = w.whole() ? -1 : 2 * (int)blockIdx.x + (w.first ? 0 : 1);
+                    mbar_arrive(&bars->item[li & 3]);
+                }
+                // The slots keep the distance in time at which an item begins: half
+                // a softmax apart each has the exponential unit to itself while
+                // the other's MMAs run.  With both first S issued together the
+                // two softmaxes overlap and a key tile takes 2.2-2.4 us instead of
+                // 1.9 (D = 128).
                 // A slot's first P V overwrites its O.  Its own epilogue of the
                 // item before is over when its softmax hands over P; after a
                 // single item the other slot's epilogue has read it as well.
@@ -419,6 +463,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     int v_stage0 = 0, v_stage1 = 0;
                     for (int t = 0; ok && t < 2 && t < n1; ++t) {
                         if (!(ok = next_tile(k_off, k_stage))) break;
+                        if (t == 1 && !FEW && !(ok = mbar_wait(&bars->p_half[0], cnt0 & 1, abort_flag))) break;
                         tc_fence_after();
                         issue_s(t ? tS1 : tS0, q_lo0, k_off);
                         mma_commit(&bars->s_full[t]);
@@ -443,12 +488,13 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                         }
                     }
                 } else {
-                    const int n0 = w.tiles_slot0(tt);   // <= n1
                     if (!(ok = next_tile(k_off, k_stage))) break;
                     tc_fence_after();
                     if (n0 > 0) {
                         issue_s(tS0, q_lo0, k_off);
                         mma_commit(&bars->s_full[0]);
+                        // slot 1 begins when slot 0's first softmax is half done (below)
+                        if (!(ok = mbar_wait(&bars->p_half[0], cnt0 & 1, abort_flag))) break;
                     }
                     issue_s(tS1, q_lo1, k_off);
                     mma_commit(&bars->s_full[1]);
@@ -464,6 +510,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                             if (j == 0 && !(ok = o_is_free(0))) break;
                             if (!(ok = pv_halves(0, cnt0 & 1, v_off, acc0))) break;
                             ++cnt0;
+                            if (j == n0 - 1) mma_commit(&bars->o_final[0]);
                         }
                         if (more) {
                             if (!(ok = next_tile(k_off, k_stage))) break;
@@ -485,14 +532,22 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                         }
                     }
                 }
-                // No slot may fall a whole phase of o_final behind (one with no
-                // key tiles in an item waits for nothing else): both have
-                // finished the item before.
-                if (ok && li > 0)
+                // A slot that handed over a P in this item has finished the item
+                // before.  One that had no key tile must not fall a whole phase
+                // of o_final behind: both slots have finished the item before.
+                const bool idle = single ? n1 == 1 : n0 == 0;
+                if (ok && idle && li > 0)
                     ok = mbar_wait(&bars->o_free[0], (li - 1) & 1, abort_flag) &&
                          mbar_wait(&bars->o_free[1], (li - 1) & 1, abort_flag);
-                if (ok) mma_commit(&bars->o_final);
+                if (ok) {
+                    if (single || idle) mma_commit(&bars->o_final[0]);
+                    mma_commit(&bars->o_final[1]);
+                }
                 prev_single = single;
+            }
+            if (ok) {
+                bars->items[li & 3].cnt = 0;
+                mbar_arrive(&bars->item[li & 3]);
             }
             mma_commit(&bars->drain);
             mbar_wait(&bars->drain, 0, nullptr);
@@ -519,35 +574,29 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         int ring = 0;       // ring tiles in front of the current item
         int n_single = 0;   // single items completed by this CTA
         int li = 0;
-        // the warp's position lives in shared memory: the key tile loop needs the registers
-        Walk& w = reinterpret_cast<Walk*>(reinterpret_cast<uint8_t*>(bars) + 1024)[warp - 2];
-        if (lane == 0) w.begin(a.s, bars, a.Hkv, tt);
-        __syncwarp();
-        auto step = [&]() {
-            __syncwarp();
-            if (lane == 0) w.next(a.s, a.Hkv, tt);
-            __syncwarp();
-        };
-        for (; ok && !w.done(); step(), ++li) {
-            const bool single = !w.two(tt);
-            const int cnt = w.t1 - w.t0;
-            const int n0 = single ? 0 : w.tiles_slot0(tt);
+        for (;; ++li) {
+            if (!(ok = wait_all(&bars->item[li & 3], (li >> 2) & 1))) break;
+            const Item& w = bars->items[li & 3];
+            const int cnt = w.cnt;
+            if (cnt == 0) break;
+            const bool single = w.single != 0;
+            const int n0 = w.n0;
             // a two-tile item's slot t owns query tile t; a single item's slots
             // own its one tile and key tiles t, t+2, ...
             const int n_mine = single ? (cnt + 1 - t) / 2 : (t ? cnt : n0);
-            const int tok0 = (2 * w.i + (single ? 0 : t)) * tt;
-            const bool valid = tok_r < tt && tok0 + tok_r < w.sq.n;
+            const int tok = w.tok0 + (single ? 0 : t * tt) + tok_r;
+            const bool valid = tok_r < tt && tok < w.n;
             const bool live = __any_sync(0xffffffffu, valid);   // rows of other lanes never meet this warp's
-            // keys the row sees, from the item's first key tile on
-            const int lim = max(0, w.sq.L - w.sq.n + min(tok0 + tok_r, w.sq.n - 1) + 1) - w.t0 * kTile;
+            // keys the row sees, from the part's first key on
+            const int lim = max(0, w.seen + min(tok, w.n - 1) + 1) - w.base;
             // from this key tile on some row of the warp is masked (uniform, so that
             // the other tiles skip the selects by a branch)
             const int mask_j = max(0, __reduce_min_sync(0xffffffffu, lim)) / kTile;
             // The key tile (of this slot, else -1) whose values behind the
             // sequence's last key are to be overwritten, and their first row.
-            const int last = (w.sq.L - 1) / kTile - w.t0;
-            const int nv = w.sq.L - (w.t0 + last) * kTile;
-            const int fix = w.sq.L > 0 && last < cnt && nv % page != 0 &&
+            const int last = (w.L - 1 - w.base) >> 7;
+            const int nv = w.L - w.base - last * kTile;
+            const int fix = w.L > 0 && last < cnt && nv % page != 0 &&
                             (single ? (last & 1) == t : t == (last < n0 ? 0 : 1)) ? last : -1;
             float m_ref = kNoKey;
             float l = 0.f;
@@ -561,10 +610,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     if (!(ok = wait_all(&bars->full[s], (c / C::kStages) & 1))) break;
                     const int stop = min(kTile, (nv + page - 1) / page * page);
                     uint8_t* tile = sRing + s * C::kTileBytes;
-                    const int chunks = (stop - nv) * 8;           // 16-byte pieces of one box
-                    for (int e = r; e < chunks * (D / 64); e += 128) {
-                        const int x = e / chunks;
-                        *reinterpret_cast<uint4*>(tile + x * C::kBoxBytes + nv * 128 + (e - x * chunks) * 16) =
+                    constexpr int kPieces = D / 8;                // 16-byte pieces of one key's values
+                    for (int e = r; e < (stop - nv) * kPieces; e += 128) {
+                        const int q = e % kPieces;
+                        *reinterpret_cast<uint4*>(tile + PageTile<D>::row(nv + e / kPieces, q >> 3) + (q & 7) * 16) =
                             make_uint4(0, 0, 0, 0);
                     }
                     fence_proxy_async_smem();
@@ -667,26 +716,21 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 w0 = t ? w_oth : w_self;
                 w1 = t ? w_self : w_oth;
             }
-            if (!(ok = wait_all(&bars->o_final, li & 1))) break;
+            if (!(ok = wait_all(&bars->o_final[t], li & 1))) break;
+            if (single && !(ok = wait_all(&bars->o_final[t ^ 1], li & 1))) break;
             tc_fence_after();
-            const bool whole = w.whole();
+            const bool whole = w.part < 0;
             const bool none = L == 0.f;     // no key in sight: O may never have been written
             const float inv = none ? 0.f : whole ? 1.f / L : 1.f;
             const float s0 = w0 * inv, s1 = w1 * inv;
-            const int orow = (w.sq.q0 + tok0 + tok_r) * a.H + w.h * G + g_r;
-            const int prow = (2 * (int)blockIdx.x + (w.first ? 0 : 1)) * 2 * tt * G + (single ? 0 : t * tt * G) + r;
-            if (valid && (!single || t == 0)) {
-                if (whole)
-                    a.lse[orow] = none ? -INFINITY : (M + __log2f(L)) * kLn2;
-                else
-                    *reinterpret_cast<float2*>(a.part_ml + 2 * (size_t)prow) = make_float2(none ? -INFINITY : M, L);
-            }
+            const int row = whole ? (w.q0 + tok) * a.H + w.h * G + g_r
+                                  : (2 * w.part + (single ? 0 : t)) * tt * G + r;
             // Rows go out through the warp's 2 KB of shared memory, 64 bytes of
             // each of the 32 rows a round: a store instruction then covers 8 rows
             // of 64 contiguous bytes, not 32 rows of 16.  16-byte pieces are
             // permuted by row against bank conflicts.
             uint8_t* stage = sStage + (warp - 2) * 2048;
-            const int dst = valid ? (whole ? orow : prow) : -1;
+            const int dst = valid ? row : -1;
             const int c_begin = single ? t * (D / 2) : 0;
             auto put = [&](int q, const uint4& v) {   // piece q of this lane's row
                 *reinterpret_cast<uint4*>(stage + lane * 64 + ((q ^ ((lane >> 1) & 3)) * 16)) = v;
@@ -702,13 +746,32 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 }
                 __syncwarp();
             };
+            auto emit = [&](const uint32_t (&x)[32], int col) {   // 32 columns of the warp's rows
+                if (whole) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        put(q, make_uint4(pack_bf16x2(__uint_as_float(x[8 * q]), __uint_as_float(x[8 * q + 1])),
+                                          pack_bf16x2(__uint_as_float(x[8 * q + 2]), __uint_as_float(x[8 * q + 3])),
+                                          pack_bf16x2(__uint_as_float(x[8 * q + 4]), __uint_as_float(x[8 * q + 5])),
+                                          pack_bf16x2(__uint_as_float(x[8 * q + 6]), __uint_as_float(x[8 * q + 7]))));
+                    store(a.o, D * 2, col * 2);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 32; c += 16) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            put(q, make_uint4(x[c + 4 * q], x[c + 4 * q + 1], x[c + 4 * q + 2], x[c + 4 * q + 3]));
+                        store(a.part_acc, D * 4, (col + c) * 4);
+                    }
+                }
+            };
             // 64 accumulators at a time: of a two-tile item 64 columns of its own O,
             // of a single item 32 columns of both O
 #pragma unroll 1
             for (int pass = 0; live && pass < D / 64; ++pass) {
-                uint32_t x[2][32];
-                tmem_ld32(single ? tmem + lane_off + 256u + c_begin + 32 * pass : tO + 64 * pass, x[0]);
-                tmem_ld32(single ? tmem + lane_off + 384u + c_begin + 32 * pass : tO + 64 * pass + 32, x[1]);
+                uint32_t x0[32], x1[32];
+                tmem_ld32(single ? tmem + lane_off + 256u + c_begin + 32 * pass : tO + 64 * pass, x0);
+                tmem_ld32(single ? tmem + lane_off + 384u + c_begin + 32 * pass : tO + 64 * pass + 32, x1);
                 tmem_wait_ld();
                 if (pass == D / 64 - 1) {   // the accumulators are free before the last rows are stored
                     tc_fence_before();
@@ -717,39 +780,26 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 if (single) {
 #pragma unroll
                     for (int c = 0; c < 32; ++c) {
-                        float f = __uint_as_float(x[0][c]) * s0;
-                        if (with1) f = fmaf(__uint_as_float(x[1][c]), s1, f);
-                        x[0][c] = __float_as_uint(none ? 0.f : f);
+                        float f = __uint_as_float(x0[c]) * s0;
+                        if (with1) f = fmaf(__uint_as_float(x1[c]), s1, f);
+                        x0[c] = __float_as_uint(none ? 0.f : f);
                     }
+                    emit(x0, c_begin + 32 * pass);
                 } else {
 #pragma unroll
                     for (int c = 0; c < 32; ++c) {
-                        x[0][c] = __float_as_uint(none ? 0.f : __uint_as_float(x[0][c]) * s0);
-                        x[1][c] = __float_as_uint(none ? 0.f : __uint_as_float(x[1][c]) * s0);
+                        x0[c] = __float_as_uint(none ? 0.f : __uint_as_float(x0[c]) * s0);
+                        x1[c] = __float_as_uint(none ? 0.f : __uint_as_float(x1[c]) * s0);
                     }
+                    emit(x0, 64 * pass);
+                    emit(x1, 64 * pass + 32);
                 }
-                const int col = single ? c_begin + 32 * pass : 64 * pass;
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    if (k == 1 && single) break;
-                    if (whole) {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            put(q, make_uint4(pack_bf16x2(__uint_as_float(x[k][8 * q]), __uint_as_float(x[k][8 * q + 1])),
-                                              pack_bf16x2(__uint_as_float(x[k][8 * q + 2]), __uint_as_float(x[k][8 * q + 3])),
-                                              pack_bf16x2(__uint_as_float(x[k][8 * q + 4]), __uint_as_float(x[k][8 * q + 5])),
-                                              pack_bf16x2(__uint_as_float(x[k][8 * q + 6]), __uint_as_float(x[k][8 * q + 7]))));
-                        store(a.o, D * 2, (col + 32 * k) * 2);
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < 32; c += 16) {
-#pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                put(q, make_uint4(x[k][c + 4 * q], x[k][c + 4 * q + 1], x[k][c + 4 * q + 2], x[k][c + 4 * q + 3]));
-                            store(a.part_acc, D * 4, (col + 32 * k + c) * 4);
-                        }
-                    }
-                }
+            }
+            if (valid && (!single || t == 0)) {
+                if (whole)
+                    a.lse[row] = none ? -INFINITY : (M + __log2f(L)) * kLn2;
+                else
+                    *reinterpret_cast<float2*>(a.part_ml + 2 * (size_t)row) = make_float2(none ? -INFINITY : M, L);
             }
             if (!live) {
                 tc_fence_before();
@@ -766,9 +816,9 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     }
 }
 
-// Joins the parts of the item that CTA blockIdx.x of the main kernel began and
+// Joins the parts of the item that share blockIdx.x of the main kernel began and
 // did not finish: the first in one of its own slots, the others in the first
-// slots of the CTAs behind it.  grid.y: slices of the item's rows.  W warps take
+// slots of the shares behind it.  grid.y: slices of the item's rows.  W warps take
 // a row, each every W-th part, a lane D / 32 head dims; the warps' results are
 // joined through shared memory (W = 8 where an item has few rows: decode cuts a
 // long cache into many parts).
@@ -776,7 +826,7 @@ constexpr int kMergeThreads = 256;
 constexpr int kMergeBatch = 4;
 
 template <int DPL, int W>
-__global__ void __launch_bounds__(kMergeThreads) paged_tc_merge_kernel(const PagedTcArgs a, int ctas) {
+__global__ void __launch_bounds__(kMergeThreads) paged_tc_merge_kernel(const PagedTcArgs a, int shares) {
     constexpr int D = 32 * DPL;
     constexpr int kRows = kMergeThreads / 32 / W;     // rows at a time
     __shared__ float s_acc[W > 1 ? W : 1][D];
@@ -785,15 +835,15 @@ __global__ void __launch_bounds__(kMergeThreads) paged_tc_merge_kernel(const Pag
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int c0 = (int)blockIdx.x;
     const int warp = (int)warp_id(), lane = (int)lane_id();
-    int slot = 2 * c0;
-    PagedPart p = a.parts[slot];
-    if (p.n_kv == 0 || p.t0 != 0) p = a.parts[++slot];
+    const PagedPart p0 = a.parts[2 * c0], p1 = a.parts[2 * c0 + 1];
+    const int slot = 2 * c0 + (p0.n_kv != 0 && p0.t0 == 0 ? 0 : 1);
+    const PagedPart p = slot == 2 * c0 ? p0 : p1;
     if (p.n_kv == 0 || p.t0 != 0 || p.t1 == p.n_kv) return;
-    // the CTA that holds the last part; with little work some CTAs between have none
-    int c1 = ctas - 1;
-    for (int c = c0 + 1; c < ctas; c += 32) {
+    // the share that holds the last part; with little work some between have none
+    int c1 = shares - 1;
+    for (int c = c0 + 1; c < shares; c += 32) {
         bool end = false;
-        if (c + lane < ctas) {
+        if (c + lane < shares) {
             const PagedPart n = a.parts[2 * (c + lane)];
             end = n.n_kv != 0 && n.t1 == n.n_kv;
         }
@@ -803,7 +853,6 @@ __global__ void __launch_bounds__(kMergeThreads) paged_tc_merge_kernel(const Pag
             break;
         }
     }
-    const Seq sq = load_seq(a.s, p.b);
     const int G = a.H / a.Hkv;
     const int rows = 2 * a.tt * G;
     const int per = (rows + (int)gridDim.y - 1) / (int)gridDim.y;
@@ -811,7 +860,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_tc_merge_kernel(const Pag
     for (int r0 = (int)blockIdx.y * per; r0 < min(rows, ((int)blockIdx.y + 1) * per); r0 += kRows) {
         const int r = r0 + warp / W;
         const int tok = p.i * 2 * a.tt + r / G;
-        if (r >= min(rows, ((int)blockIdx.y + 1) * per) || tok >= sq.n) break;   // W > 1: the same for all warps
+        if (r >= min(rows, ((int)blockIdx.y + 1) * per) || tok >= p.n) break;   // W > 1: the same for all warps
         float M = -INFINITY, L = 0.f, A[DPL];
 #pragma unroll
         for (int i = 0; i < DPL; ++i) A[i] = 0.f;
@@ -864,7 +913,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_tc_merge_kernel(const Pag
             }
         }
         const float inv = L == 0.f ? 0.f : 1.f / L;
-        const size_t row = (size_t)(sq.q0 + tok) * a.H + p.h * G + r % G;
+        const size_t row = (size_t)(p.q0 + tok) * a.H + p.h * G + r % G;
         uint16_t* out = static_cast<uint16_t*>(a.o) + row * D + lane * DPL;
 #pragma unroll
         for (int i = 0; i < DPL; i += 2)
@@ -892,7 +941,7 @@ cudaError_t launch_d(const PagedTcArgs& a, int sm_count, cudaStream_t stream) {
     if ((e = cudaLaunchKernelEx(&cfg, kern, a.tm_q, a.tm_k, a.tm_v, a)) != cudaSuccess) return e;
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const int rows = 2 * a.tt * (a.H / a.Hkv);
-    cfg.gridDim = dim3((unsigned)sm_count, (unsigned)(FEW ? 1 : (rows + 31) / 32));
+    cfg.gridDim = dim3((unsigned)sm_count, (unsigned)(FEW ? 1 : (rows + 15) / 16));
     cfg.blockDim = dim3(kMergeThreads);
     cfg.dynamicSmemBytes = 0;
     e = cudaLaunchKernelEx(&cfg, paged_tc_merge_kernel<D / 32, FEW ? 8 : 1>, a, sm_count);

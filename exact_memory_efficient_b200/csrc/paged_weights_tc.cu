@@ -262,11 +262,8 @@ paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         }
         const int shift = a.s.page_shift;
         const int box_rows = min(kTile, 1 << shift);
-        constexpr int kHalves = D / 64;
-        const int boxes = kTile / box_rows * kHalves;
-        const int my_row = (int)lane / kHalves * box_rows;
-        const int my_half = (int)lane % kHalves;
-        const bool mine = (int)lane < boxes;
+        const int my_row = (int)lane * box_rows;         // first key of the lane's box in the tile
+        const bool mine = my_row < kTile;
         const int outside = a.s.num_pages * a.Hkv;
         int li = 0, qc = 0;         // items and Q tiles asked for
         bool ok = true;
@@ -296,8 +293,8 @@ paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                 int z = outside;
                 if (mine && key < w.sq.L) z = load_page(a.s, w.b, key >> shift) * a.Hkv + w.h;
                 if (mine)
-                    tma_load_3d(sK + (2 * ks + t) * C::kTileBytes + my_half * C::kBoxBytes + my_row * 128, &tm_k,
-                                &bars->k_full[ks], my_half * 64, key & ((1 << shift) - 1), z);
+                    tma_load_5d(sK + (2 * ks + t) * C::kTileBytes + PageTile<D>::row(my_row, 0), &tm_k,
+                                &bars->k_full[ks], 0, 0, 0, (key & ((1 << shift) - 1)) >> 3, z);
             }
             ++li;
             const int f = first_tile(w.sq, tt, w.i);
@@ -316,7 +313,7 @@ paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                 if (qc >= C::kQStages && !(ok = wait(&bars->q_empty[s], (qc / C::kQStages - 1) & 1))) break;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(&bars->q_full[s], (unsigned)(G * tt * D * 2));
-                    for (int x = 0; x < kHalves; ++x)
+                    for (int x = 0; x < D / 64; ++x)
                         tma_load_3d(sQ + s * C::kTileBytes + x * C::kBoxBytes, &tm_q, &bars->q_full[s], x * 64, w.h * G,
                                     w.sq.q0 + tok0);
                 }
@@ -357,8 +354,9 @@ paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                         tc_fence_after();
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk)
-                            mma_ss_lo(tmem + (unsigned)(t * 256 + buf * 128), k_lo + (2 * ks + t) * kStep + kmajor_step(kk),
-                                      q_lo + s * kStep + kmajor_step(kk), idesc, kk > 0);
+                            mma_ss_desc(tmem + (unsigned)(t * 256 + buf * 128),
+                                        k_lo + (2 * ks + t) * kStep + PageTile<D>::kmajor(kk), PageTile<D>::kHi,
+                                        q_lo + s * kStep + kmajor_step(kk), kDescHiSw128, idesc, kk > 0);
                         mma_commit(&bars->s_full[t][buf]);
                         if (t) ++cnt1; else ++cnt0;
                     }
