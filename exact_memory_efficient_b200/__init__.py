@@ -480,31 +480,30 @@ def _bad(where: str, what: str):
     raise MeaError(MEA_ERR_INVALID_ARG, f"{where}: {what}")
 
 
-def _same_device(where: str, first, named) -> None:
-    """Every tensor on ``first``'s CUDA device; all but the packed ones dense, of the given dtype."""
-    dev = first.device
-    if dev.type != "cuda":
+def _same_device(where: str, first, named) -> int:
+    """Index of ``first``'s CUDA device; every other tensor on it, dense and of the given dtype."""
+    dev = first.get_device()
+    if dev < 0:
         _bad(where, "CUDA tensors")
     for name, t, dtype in named:
-        if t is None:
-            continue
-        if t.device != dev:
-            _bad(where, f"{name} is not on the device of the first tensor")
-        if t.dtype != dtype:
-            _bad(where, f"{name} must be {dtype}")
-        if not t.is_contiguous():
-            _bad(where, f"{name} must be contiguous")
+        if t is not None and (t.get_device() != dev or t.dtype != dtype or not t.is_contiguous()):
+            if t.get_device() != dev:
+                _bad(where, f"{name} is not on the device of the first tensor")
+            _bad(where, f"{name} must be {dtype}" if t.dtype != dtype else f"{name} must be contiguous")
+    return dev
 
 
 def _packed(where: str, name: str, t, dtype, T=None, heads=None, D=None) -> int:
     """Token stride of packed [T, heads, D] rows: heads and dims dense, any token stride."""
-    if t.dim() != 3 or t.dtype != dtype or (T is not None and t.shape[0] != T) or \
-            (heads is not None and t.shape[1] != heads) or (D is not None and t.shape[2] != D):
+    if t.dim() != 3 or t.dtype != dtype:
         _bad(where, f"{name} shape/dtype mismatch")
     n, h, d = t.shape
-    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+    if (T is not None and n != T) or (heads is not None and h != heads) or (D is not None and d != D):
+        _bad(where, f"{name} shape/dtype mismatch")
+    token, head, dim = t.stride()
+    if (d > 1 and dim != 1) or (h > 1 and head != d):
         _bad(where, f"{name}: heads and head dims must be dense")
-    return t.stride(0) if n > 1 else h * d
+    return token if n > 1 else h * d
 
 
 def _pages(where: str, k_cache, v_cache=None, weights=None, like=None):
@@ -528,21 +527,31 @@ def _batch(where: str, kv_len, page_table, cu_q=None):
     return page_table.shape
 
 
-def _launch(where: str, fn, device, stream, *args) -> None:
-    """fn(*args, stream) with ``device`` current (its current stream where none is given)."""
-    with _on(device):
-        st = fn(*args, _stream_handle(stream))
-    _check(st, where)
+def _launch(where: str, fn, device: int, stream, *args) -> None:
+    """fn(*args, stream) with the device current (its current stream where none is given)."""
+    if device != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _launch(where, fn, device, stream, *args)
+    st = fn(*args, _raw_stream(device) if stream is None else _stream_handle(stream))
+    if st != MEA_OK:
+        raise MeaError(st, where)
 
 
-def _allocating(stream, device):
-    """Context in which outputs and scratch of a call on ``stream`` are allocated: on that stream, so
-    that the allocator does not hand their memory on while the call may still run."""
+def _raw_stream(device: int) -> int:
+    """Handle of the device's current stream (without building a torch.cuda.Stream for it: 0.1 against 3 us)."""
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return int(get(device)) if get is not None else int(torch.cuda.current_stream(device).cuda_stream)
+
+
+def _empty(stream, like, *shapes):
+    """Tensors of the (shape, dtype) pairs on ``like``'s device, allocated on ``stream`` where one is
+    given, so that the allocator does not hand their memory on while the call may still run."""
     if stream is None:
-        return contextlib.nullcontext()
+        return [like.new_empty(shape, dtype=dtype) if shape is not None else None for shape, dtype in shapes]
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(_stream_handle(stream), device=device)
-    return torch.cuda.stream(stream)
+        stream = torch.cuda.ExternalStream(_stream_handle(stream), device=like.device)
+    with torch.cuda.stream(stream):
+        return _empty(None, like, *shapes)
 
 
 def mea_rope(x, y, positions, freq, layout: int = MEA_ROPE_HALF, mscale: float = 1.0, inverse: bool = False,
@@ -556,17 +565,16 @@ def mea_rope(x, y, positions, freq, layout: int = MEA_ROPE_HALF, mscale: float =
         _bad("mea_rope", "freq must be [rot_dim / 2]")
     if tuple(positions.shape) not in ((N,), (B, N)):
         _bad("mea_rope", "positions must be [N] or [B, N]")
-    _same_device("mea_rope", x, (("x", x, x.dtype), ("y", y, x.dtype), ("positions", positions, torch.int32),
-                                 ("freq", freq, torch.float64)))
-    _launch("mea_rope", load_library().mea_rope, x.device, stream, _ptr(x), _ptr(y), _ptr(positions), _ptr(freq), B, H,
+    dev = _same_device("mea_rope", x, (("x", x, x.dtype), ("y", y, x.dtype), ("positions", positions, torch.int32),
+                                       ("freq", freq, torch.float64)))
+    _launch("mea_rope", load_library().mea_rope, dev, stream, _ptr(x), _ptr(y), _ptr(positions), _ptr(freq), B, H,
             N, D, 2 * freq.shape[0], int(positions.dim() == 2), int(layout), float(mscale), int(bool(inverse)),
             _dtype_code(x))
 
 
 def rope(x, positions, freq, interleaved: bool = False, mscale: float = 1.0, inverse: bool = False, stream=None):
     """Allocate y with torch and run ``mea_rope``; the gradient of x is ``rope(dy, ..., inverse=True)``."""
-    with _allocating(stream, x.device):
-        y = torch.empty_like(x, memory_format=torch.contiguous_format)
+    y, = _empty(stream, x, (x.shape, x.dtype))
     mea_rope(x, y, positions, freq, MEA_ROPE_INTERLEAVED if interleaved else MEA_ROPE_HALF, mscale, inverse, stream)
     return y
 
@@ -594,13 +602,13 @@ def mea_paged_append(q, q_out, k, v, k_cache, v_cache, weights, cu_q, kv_len, pa
         _bad(w, "positions must be [T]")
     if freq is not None and freq.dim() != 1:
         _bad(w, "freq must be [rot_dim / 2]")
-    _same_device(w, k, (("k_cache", k_cache, dt), ("v_cache", v_cache, dt), ("weights", weights, torch.float32),
+    dev = _same_device(w, k, (("k_cache", k_cache, dt), ("v_cache", v_cache, dt), ("weights", weights, torch.float32),
                         ("cu_q", cu_q, torch.int32), ("kv_len", kv_len, torch.int32),
                         ("page_table", page_table, torch.int32), ("positions", positions, torch.int32),
                         ("freq", freq, torch.float64), ("q_out", q_out, dt)))
-    if v.device != k.device or (q is not None and q.device != k.device):
+    if v.get_device() != dev or (q is not None and q.get_device() != dev):
         _bad(w, "q, k and v must be on one device")
-    _launch(w, load_library().mea_paged_append, k.device, stream, _ptr(q), _ptr(q_out), _ptr(k), _ptr(v),
+    _launch(w, load_library().mea_paged_append, dev, stream, _ptr(q), _ptr(q_out), _ptr(k), _ptr(v),
             _ptr(k_cache), _ptr(v_cache), _ptr(weights), _ptr(cu_q), _ptr(kv_len), _ptr(page_table), _ptr(positions),
             _ptr(freq), T, B, H, Hkv, D, qs, ks, vs, pages, page, max_pages, 0 if freq is None else 2 * freq.shape[0],
             int(layout), float(mscale), _dtype_code(k_cache))
@@ -610,10 +618,7 @@ def paged_append(q, k, v, k_cache, v_cache, weights, cu_q, kv_len, page_table, p
                  interleaved: bool = False, mscale: float = 1.0, stream=None):
     """Allocate the turned q with torch and run ``mea_paged_append``; returns it (None without q).  Rows
     outside every sequence are not written."""
-    q_out = None
-    if q is not None:
-        with _allocating(stream, q.device):
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    q_out = None if q is None else _empty(stream, q, (q.shape, q.dtype))[0]
     mea_paged_append(q, q_out, k, v, k_cache, v_cache, weights, cu_q, kv_len, page_table, positions, freq,
                      MEA_ROPE_INTERLEAVED if interleaved else MEA_ROPE_HALF, mscale, stream)
     return q_out
@@ -640,15 +645,15 @@ def mea_attn_paged_weights_workspace_size(T: int, B: int, H: int, H_kv: int, D: 
                             (T, B, H, H_kv, D, max_q, max_kv), dtype)
 
 
-def _on(device):
-    """Context with ``device`` current (nothing to do where it is)."""
-    return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+def _on(t):
+    """Context with ``t``'s device current (nothing to do where it is)."""
+    return contextlib.nullcontext() if t.get_device() == torch.cuda.current_device() else torch.cuda.device(t.device)
 
 
-def _workspace_bytes(where: str, workspace, device) -> int:
+def _workspace_bytes(where: str, workspace, device: int) -> int:
     if workspace is None:
         return 0
-    if workspace.device != device or not workspace.is_contiguous():
+    if workspace.get_device() != device or not workspace.is_contiguous():
         _bad(where, "workspace must be a contiguous tensor on the device")
     return workspace.numel() * workspace.element_size()
 
@@ -665,11 +670,11 @@ def mea_attn_paged(q, k_cache, v_cache, o, lse, cu_q, kv_len, page_table, max_q:
     T, H = q.shape[:2]
     if o.shape != q.shape or tuple(lse.shape) != (T, H):
         _bad(w, "o must be shaped like q, lse [T, H]")
-    _same_device(w, q, (("k_cache", k_cache, dt), ("v_cache", v_cache, dt), ("o", o, dt), ("lse", lse, torch.float32),
+    dev = _same_device(w, q, (("k_cache", k_cache, dt), ("v_cache", v_cache, dt), ("o", o, dt), ("lse", lse, torch.float32),
                         ("cu_q", cu_q, torch.int32), ("kv_len", kv_len, torch.int32),
                         ("page_table", page_table, torch.int32)))
-    ws_bytes = _workspace_bytes(w, workspace, q.device)
-    _launch(w, load_library().mea_attn_paged, q.device, stream, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(o),
+    ws_bytes = _workspace_bytes(w, workspace, dev)
+    _launch(w, load_library().mea_attn_paged, dev, stream, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(o),
             _ptr(lse), _ptr(cu_q), _ptr(kv_len), _ptr(page_table), T, B, H, Hkv, D, qs, pages, page, max_pages,
             int(max_q), int(max_kv), float(scale), _dtype_code(q), _ptr(workspace), ws_bytes)
 
@@ -686,12 +691,9 @@ def attention_paged(q, k_cache, v_cache, cu_q, kv_len, page_table, max_q: int, m
     if scale is None:
         scale = 1.0 / math.sqrt(q.shape[-1])
     T, H, D = q.shape
-    with _on(q.device):
+    with _on(q):
         n = mea_attn_paged_workspace_size(T, kv_len.shape[0], H, k_cache.shape[1], D, max_q, max_kv, q.dtype)
-    with _allocating(stream, q.device):
-        o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
-        ws = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+    o, lse, ws = _empty(stream, q, (q.shape, q.dtype), ((T, H), torch.float32), ((n,) if n else None, torch.uint8))
     mea_attn_paged(q, k_cache, v_cache, o, lse, cu_q, kv_len, page_table, max_q, max_kv, scale, ws, stream)
     return o, lse
 
@@ -708,13 +710,13 @@ def mea_attn_paged_weights(q, lse, k_cache, weights, cu_q, kv_len, page_table, m
     T, H = q.shape[:2]
     if tuple(lse.shape) != (T, H):
         _bad(w, "lse must be [T, H]")
-    _same_device(w, q, (("k_cache", k_cache, k_cache.dtype), ("weights", weights, torch.float32),
+    dev = _same_device(w, q, (("k_cache", k_cache, k_cache.dtype), ("weights", weights, torch.float32),
                         ("lse", lse, torch.float32), ("cu_q", cu_q, torch.int32), ("kv_len", kv_len, torch.int32),
                         ("page_table", page_table, torch.int32)))
-    _launch(w, load_library().mea_attn_paged_weights, q.device, stream, _ptr(q), _ptr(lse), _ptr(k_cache),
+    _launch(w, load_library().mea_attn_paged_weights, dev, stream, _ptr(q), _ptr(lse), _ptr(k_cache),
             _ptr(weights), _ptr(cu_q), _ptr(kv_len), _ptr(page_table), T, B, H, Hkv, D, qs, pages, page, max_pages,
             int(max_q), int(max_kv), float(scale), _dtype_code(q), _ptr(workspace),
-            _workspace_bytes(w, workspace, q.device))
+            _workspace_bytes(w, workspace, dev))
 
 
 def attention_paged_weights(q, lse, k_cache, weights, cu_q, kv_len, page_table, max_q: int, max_kv: int,
@@ -726,10 +728,9 @@ def attention_paged_weights(q, lse, k_cache, weights, cu_q, kv_len, page_table, 
     if not q.is_cuda:
         _bad("attention_paged_weights", "CUDA tensors")
     T, H, D = q.shape
-    with _on(q.device):
+    with _on(q):
         n = mea_attn_paged_weights_workspace_size(T, kv_len.shape[0], H, k_cache.shape[1], D, max_q, max_kv, q.dtype)
-    with _allocating(stream, q.device):
-        ws = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+    ws, = _empty(stream, q, ((n,) if n else None, torch.uint8))
     mea_attn_paged_weights(q, lse, k_cache, weights, cu_q, kv_len, page_table, max_q, max_kv,
                            1.0 / math.sqrt(D) if scale is None else scale, ws, stream)
 
@@ -748,11 +749,11 @@ def mea_paged_evict(k_cache, v_cache, weights, page_table, kv_len, dst_table, kv
     if kv_len_out is not None and kv_len_out.shape != kv_len.shape:
         _bad(w, "kv_len_out must be [B]")
     i32 = torch.int32
-    _same_device(w, k_cache, (("k_cache", k_cache, k_cache.dtype), ("v_cache", v_cache, k_cache.dtype),
+    dev = _same_device(w, k_cache, (("k_cache", k_cache, k_cache.dtype), ("v_cache", v_cache, k_cache.dtype),
                               ("weights", weights, torch.float32), ("page_table", page_table, i32),
                               ("kv_len", kv_len, i32), ("dst_table", dst_table, i32), ("keep_idx", keep_idx, i32),
                               ("kv_len_out", kv_len_out, i32)))
-    _launch(w, load_library().mea_paged_evict, k_cache.device, stream, _ptr(k_cache), _ptr(v_cache), _ptr(weights),
+    _launch(w, load_library().mea_paged_evict, dev, stream, _ptr(k_cache), _ptr(v_cache), _ptr(weights),
             _ptr(page_table), _ptr(kv_len), _ptr(dst_table), _ptr(kv_len_out), _ptr(keep_idx), B, Hkv, D, pages, page,
             max_pages, dst_table.shape[1], keep_idx.shape[2], int(n_recent), _dtype_code(k_cache))
 
@@ -762,9 +763,10 @@ def paged_evict(k_cache, v_cache, weights, page_table, kv_len, dst_table, n_keep
     _pages("paged_evict", k_cache)
     if n_keep < 1:
         _bad("paged_evict", "n_keep below 1")
-    with _allocating(stream, k_cache.device):
-        idx = torch.empty((kv_len.shape[0], k_cache.shape[1], n_keep), dtype=torch.int32, device=k_cache.device)
-        out = torch.empty_like(kv_len)
+    if not k_cache.is_cuda:
+        _bad("paged_evict", "CUDA tensors")
+    B = kv_len.shape[0]
+    idx, out = _empty(stream, k_cache, ((B, k_cache.shape[1], n_keep), torch.int32), ((B,), torch.int32))
     mea_paged_evict(k_cache, v_cache, weights, page_table, kv_len, dst_table, out, idx, n_recent, stream)
     return idx, out
 
