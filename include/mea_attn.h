@@ -404,7 +404,7 @@ mea_status_t mea_attn_bwd_noalloc(const void* q, const void* k, const void* v,
  *    multiples of 8 and at least heads * D.  o [T, H, D] and lse [T, H] (fp32)
  *    are dense.  Sequence b owns the rows cu_q[b] <= t < cu_q[b + 1]; cu_q
  *    [B + 1] int32 is not decreasing and at most T.  Rows outside every
- *    sequence are neither read nor written.
+ *    sequence may hold anything and are not written.
  *  - The cache is num_pages pages of page_size keys (16, 32, 64, 128 or 256):
  *    k_cache, v_cache [num_pages, H_kv, page_size, D], and, where it is
  *    bounded, weights [num_pages, H_kv, page_size] fp32.
