@@ -271,7 +271,18 @@ paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             const int got = lane != 0 || mbar_wait(bar, parity, abort_flag);
             return __shfl_sync(0xffffffffu, got, 0) != 0;
         };
-        for (; ok && !w.done(); w.next(a)) {
+        // page coordinates of the lane's boxes in an item's two key tiles, looked up
+        // an item ahead: a lookup takes about half as long as the item's K
+        int z[2] = {outside, outside}, z_next[2];
+        auto look_up = [&](const Walk& x, int (&at)[2]) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int key = (2 * x.i + t) * kTile + my_row;
+                at[t] = mine && key < x.sq.L ? load_page(a.s, x.b, key >> shift) * a.Hkv + x.h : outside;
+            }
+        };
+        if (!w.done()) look_up(w, z);
+        while (ok && !w.done()) {
             const int ks = li & 1;
             const int n_kt = w.two() ? 2 : 1;
             if (li >= 2 && !(ok = wait(&bars->k_empty[ks], ((li >> 1) - 1) & 1))) break;
@@ -288,14 +299,18 @@ paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                 mbar_arrive_expect_tx(&bars->k_full[ks], (unsigned)(n_kt * C::kTileBytes));
             }
             __syncwarp();
-            for (int t = 0; t < n_kt; ++t) {
-                const int key = (2 * w.i + t) * kTile + my_row;
-                int z = outside;
-                if (mine && key < w.sq.L) z = load_page(a.s, w.b, key >> shift) * a.Hkv + w.h;
-                if (mine)
-                    tma_load_5d(sK + (2 * ks + t) * C::kTileBytes + PageTile<D>::row(my_row, 0), &tm_k,
-                                &bars->k_full[ks], 0, 0, 0, (key & ((1 << shift) - 1)) >> 3, z);
+            if (mine) {
+                const int group = ((2 * w.i * kTile + my_row) & ((1 << shift) - 1)) >> 3;
+                tma_load_5d(sK + 2 * ks * C::kTileBytes + PageTile<D>::row(my_row, 0), &tm_k, &bars->k_full[ks], 0, 0, 0,
+                            group, z[0]);
+                if (n_kt == 2)
+                    tma_load_5d(sK + (2 * ks + 1) * C::kTileBytes + PageTile<D>::row(my_row, 0), &tm_k,
+                                &bars->k_full[ks], 0, 0, 0,
+                                (((2 * w.i + 1) * kTile + my_row) & ((1 << shift) - 1)) >> 3, z[1]);
             }
+            Walk ahead = w;
+            ahead.next(a);
+            if (!ahead.done()) look_up(ahead, z_next);
             ++li;
             const int f = first_tile(w.sq, tt, w.i);
             for (int u = w.u0; ok && u < w.u1; ++u) {
@@ -323,6 +338,9 @@ paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                 if (lane == 0) mbar_arrive(&bars->q_full[s]);
                 ++qc;
             }
+            w = ahead;
+            z[0] = z_next[0];
+            z[1] = z_next[1];
         }
         // never leave with copies in flight
         for (int i = li > 2 ? li - 2 : 0; i < li; ++i) mbar_wait(&bars->k_full[i & 1], (i >> 1) & 1, nullptr);
