@@ -15,12 +15,16 @@
 // workspace slot, to be added in order by weights_merge_kernel; without it (one
 // query tile per item: decode) a CTA takes the items that begin in its share.
 //
-// Roles (320 threads): warp 0 TMA producer (K pair per item, Q tile and its
-// rows' lse per unit), warp 1 MMA issuer, warps 2-5 and 6-9 the two key tiles.
+// Roles (608 threads): warp 0 TMA producer of K (a pair of tiles per item), warp
+// 18 of Q (a tile per unit, with its rows' lse), warp 1 MMA issuer; of the two key
+// tiles each has eight warps, four for the first 64 columns of every unit and
+// four for the others, whose sums are added at the item's end.
 // TMEM: two score buffers of 128 columns per key tile.
 //
 // Bound: decode reads K once (HBM); with many rows one exponential per score
-// binds (16 per clock and SM), the tensor cores need half that time.
+// binds (16 per clock and SM), the tensor cores need half that time.  With four
+// warps per key tile every warp waited for the same barriers at the same time
+// and the exponential unit idled meanwhile.
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -33,30 +37,44 @@ namespace mea {
 namespace {
 
 constexpr int kTile = 128;
-constexpr int kThreads = 320;
+constexpr int kThreads = 608;         // 19 warps
+constexpr int kQWarp = 18;
 constexpr float kLog2e = 1.4426950408889634f;
 
-template <int D>
+// FEW: at most kFewRows rows per query tile (decode).  Q then takes 2 KB per 64
+// head dims and the space goes to K: three pairs in flight instead of two at
+// D = 128 (six at D = 64), since decode is bound by the bytes in flight.
+constexpr int kFewRows = 16;
+constexpr int kMaxPairs = 6;
+
+template <int D, bool FEW>
 struct Cfg {
     static constexpr int kTileBytes = kTile * D * 2;
-    static constexpr int kBoxBytes = 128 * 128;
-    static constexpr int kPairs = 2;                          // K pairs in flight
-    static constexpr int kQStages = D == 128 ? 2 : 4;
-    static constexpr int kSmemData = (2 * kPairs + kQStages) * kTileBytes;
+    static constexpr int kQBox = FEW ? kFewRows * 128 : 128 * 128;   // 64 head dims of a query tile
+    static constexpr int kQBytes = D / 64 * kQBox;
+    static constexpr int kPairs = FEW ? (D == 128 ? 3 : 6) : 2;      // K pairs in flight
+    static constexpr int kQStages = D == 128 && !FEW ? 2 : 4;
+    static constexpr int kSmemData = 2 * kPairs * kTileBytes + kQStages * kQBytes;
     static constexpr int kLseBytes = kQStages * kTile * 4;
-    static constexpr int kSmemBytes = kSmemData + kLseBytes + 1024 /*barriers*/ + 1024 /*alignment slack*/;
-    static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+    static constexpr int kSumBytes = 2 * kTile * 4;          // the second halves' sums
+    static constexpr int kSmemBytes = kSmemData + kLseBytes + kSumBytes + 1024 /*barriers*/ + 1024 /*alignment slack*/;
+    static_assert(kSmemBytes <= 227 * 1024 && kPairs <= kMaxPairs, "shared memory");
 };
 
 struct Barriers {
-    uint64_t k_full[2], k_empty[2];
+    uint64_t k_full[kMaxPairs], k_empty[kMaxPairs];
     uint64_t q_full[4], q_empty[4];
     uint64_t s_full[2][2], s_free[2][2];   // [key tile][buffer]
+    uint64_t sum_full[8], sum_free[8];     // [key tile, quarter of it]
     uint64_t drain;
     unsigned tmem_base;
     int abort_flag;
-    int b0, h0, i0, u0;
-    long long units;
+    // this CTA's share: where it begins, and its units
+    struct Share {
+        Seq sq;
+        int b, h, i, u0;
+        long long units;
+    } share;
     long long warp_sum[kThreads / 32];
 };
 
@@ -64,7 +82,8 @@ __device__ __forceinline__ int q_tiles(const Seq& sq, int tt) { return (sq.n + t
 __device__ __forceinline__ int items_of(const Seq& sq) { return sq.n > 0 ? (sq.L + 2 * kTile - 1) / (2 * kTile) : 0; }
 // first query tile of item i: the one of the first token that sees key 256 i
 __device__ __forceinline__ int first_tile(const Seq& sq, int tt, int i) {
-    return max(0, i * 2 * kTile - (sq.L - sq.n)) / tt;
+    const int first = i * 2 * kTile - (sq.L - sq.n);
+    return first < tt ? 0 : first / tt;
 }
 __device__ __forceinline__ int units_of(const Seq& sq, int tt, int i) { return q_tiles(sq, tt) - first_tile(sq, tt, i); }
 // items that every query tile sees
@@ -80,15 +99,15 @@ struct Walk {
     bool first, split;
 
     __device__ __forceinline__ void begin(const PagedWeightsTcArgs& a, const Barriers* bars) {
-        b = bars->b0;
-        h = bars->h0;
-        i = bars->i0;
-        u0 = bars->u0;
-        left = bars->units;
+        sq = bars->share.sq;
+        b = bars->share.b;
+        h = bars->share.h;
+        i = bars->share.i;
+        u0 = bars->share.u0;
+        left = bars->share.units;
         first = true;
         split = a.split;
         if (left <= 0) return;
-        sq = load_seq(a.s, b);
         items = items_of(sq);
         n_units = units_of(sq, a.tt, i);
         u1 = split ? (int)min((long long)n_units, u0 + left) : n_units;
@@ -125,8 +144,9 @@ struct Walk {
 __device__ __forceinline__ void find_share(const PagedWeightsTcArgs& a, Barriers* bars) {
     const int tid = (int)threadIdx.x;
     const unsigned lane = lane_id(), warp = warp_id();
+    Seq sq;
     auto of_seq = [&](int b) {
-        const Seq sq = load_seq(a.s, b);
+        sq = load_seq(a.s, b);
         const int items = items_of(sq), full = full_items(sq);
         long long sum = (long long)full * q_tiles(sq, a.tt);
         for (int i = full; i < items; ++i) sum += units_of(sq, a.tt, i);
@@ -161,16 +181,17 @@ __device__ __forceinline__ void find_share(const PagedWeightsTcArgs& a, Barriers
     }
     const long long c = blockIdx.x, C = gridDim.x;
     const long long w0 = W * c / C, w1 = W * (c + 1) / C;
-    if (tid == 0) bars->units = w1 - w0;
+    if (tid == 0) bars->share.units = w1 - w0;
     auto locate = [&](int b, long long before, long long sum) {
         if (w0 < before || w0 >= before + sum || w1 <= w0) return;
-        const Seq sq = load_seq(a.s, b);
-        const int items = items_of(sq), full = full_items(sq), nq = q_tiles(sq, a.tt);
+        const int items = items_of(sq), full = full_items(sq), nq = q_tiles(sq, a.tt);   // sq is b's since of_seq(b)
         const long long per_head = sum / a.Hkv;
         long long x = w0 - before;
-        bars->b0 = b;
-        bars->h0 = (int)(x / per_head);
-        x -= bars->h0 * per_head;
+        Barriers::Share& at = bars->share;
+        at.sq = sq;
+        at.b = b;
+        at.h = (int)(x / per_head);
+        x -= at.h * per_head;
         int i = (int)min((long long)full, x / nq);
         x -= (long long)i * nq;
         for (; i >= full && i + 1 < items; ++i) {
@@ -178,8 +199,8 @@ __device__ __forceinline__ void find_share(const PagedWeightsTcArgs& a, Barriers
             if (x < n) break;
             x -= n;
         }
-        bars->i0 = i;
-        bars->u0 = (int)x;
+        at.i = i;
+        at.u0 = (int)x;
     };
     if (a.s.B <= kThreads) {
         if (tid < a.s.B) locate(tid, block_before, mine);
@@ -197,39 +218,68 @@ __device__ __forceinline__ void find_share(const PagedWeightsTcArgs& a, Barriers
     __syncthreads();
 }
 
+// Pairs of fp32 in one instruction each, every lane rounded as fmaf and a sum.
+__device__ __forceinline__ void scale_pair(float& d0, float& d1, float x0, float x1, float c, float a0, float a1) {
+    asm("{\n\t.reg .b64 px, pc, pa, pd;\n\t"
+        "mov.b64 px, {%2, %3};\n\t"
+        "mov.b64 pc, {%4, %4};\n\t"
+        "mov.b64 pa, {%5, %6};\n\t"
+        "fma.rn.f32x2 pd, px, pc, pa;\n\t"
+        "mov.b64 {%0, %1}, pd;\n\t}"
+        : "=f"(d0), "=f"(d1)
+        : "f"(x0), "f"(x1), "f"(c), "f"(a0), "f"(a1));
+}
+__device__ __forceinline__ void add_pair(float& d0, float& d1, float x0, float x1) {
+    asm("{\n\t.reg .b64 px, pd;\n\t"
+        "mov.b64 px, {%2, %3};\n\t"
+        "mov.b64 pd, {%0, %1};\n\t"
+        "add.rn.f32x2 pd, pd, px;\n\t"
+        "mov.b64 {%0, %1}, pd;\n\t}"
+        : "+f"(d0), "+f"(d1)
+        : "f"(x0), "f"(x1));
+}
+
 // Slot of key `key` of (b, h) in weights.
 __device__ __forceinline__ size_t weight_at(const PagedBatch& s, int Hkv, int b, int h, int key) {
     return (((size_t)load_page(s, b, key >> s.page_shift) * Hkv + h) << s.page_shift) + (key & ((1 << s.page_shift) - 1));
 }
 
-template <int D>
+template <int D, bool FEW>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const PagedWeightsTcArgs a) {
-    using C = Cfg<D>;
+    using C = Cfg<D, FEW>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t* sK = smem;                                       // [pair][key tile]
     uint8_t* sQ = smem + 2 * C::kPairs * C::kTileBytes;
-    float* sLse = reinterpret_cast<float*>(smem + C::kSmemData);   // [Q stage][row], times log2 e
-    Barriers* bars = reinterpret_cast<Barriers*>(smem + C::kSmemData + C::kLseBytes);
+    float* sLse = reinterpret_cast<float*>(smem + C::kSmemData);   // [Q stage][row], times -log2 e
+    float* sSum = reinterpret_cast<float*>(smem + C::kSmemData + C::kLseBytes);
+    Barriers* bars = reinterpret_cast<Barriers*>(smem + C::kSmemData + C::kLseBytes + C::kSumBytes);
+    static_assert(sizeof(Barriers) <= 1024, "shared memory");
     const unsigned warp = warp_id();
     const unsigned lane = lane_id();
     const int tt = a.tt;
     const int G = a.H / a.Hkv;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < C::kPairs; ++i) {
             mbar_init(&bars->k_full[i], 1);
             mbar_init(&bars->k_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
             for (int j = 0; j < 2; ++j) {
                 mbar_init(&bars->s_full[i][j], 1);
-                mbar_init(&bars->s_free[i][j], 128);
+                mbar_init(&bars->s_free[i][j], 256);
             }
         }
         for (int i = 0; i < C::kQStages; ++i) {
             mbar_init(&bars->q_full[i], 2);    // the copies, and the rows' lse
-            mbar_init(&bars->q_empty[i], 257);   // both MMAs, and the readers of lse
+            mbar_init(&bars->q_empty[i], 513);   // both MMAs, and the readers of lse
+        }
+        for (int i = 0; i < 8; ++i) {
+            mbar_init(&bars->sum_full[i], 32);
+            mbar_init(&bars->sum_free[i], 32);
         }
         mbar_init(&bars->drain, 1);
         bars->abort_flag = 0;
@@ -238,6 +288,10 @@ paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     if (warp == 0) {
         tmem_alloc(&bars->tmem_base, 512);
         tmem_relinquish();
+        if (lane == 0) {   // kernel parameters: no need to wait for the kernel in front
+            prefetch_tmap(&tm_q);
+            prefetch_tmap(&tm_k);
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -252,20 +306,16 @@ paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     w.begin(a, bars);
     if (warp == 0) {
         // ------------------------------------------------ producer
-        if (lane == 0) {
-            prefetch_tmap(&tm_q);
-            prefetch_tmap(&tm_k);
-            if (a.split) {
-                a.parts[2 * blockIdx.x].n_kv = 0;
-                a.parts[2 * blockIdx.x + 1].n_kv = 0;
-            }
+        if (lane == 0 && a.split) {
+            a.parts[2 * blockIdx.x].n_kv = 0;
+            a.parts[2 * blockIdx.x + 1].n_kv = 0;
         }
         const int shift = a.s.page_shift;
         const int box_rows = min(kTile, 1 << shift);
         const int my_row = (int)lane * box_rows;         // first key of the lane's box in the tile
         const bool mine = my_row < kTile;
         const int outside = a.s.num_pages * a.Hkv;
-        int li = 0, qc = 0;         // items and Q tiles asked for
+        int li = 0;                 // items asked for
         bool ok = true;
         auto wait = [&](uint64_t* bar, unsigned parity) -> bool {
             const int got = lane != 0 || mbar_wait(bar, parity, abort_flag);
@@ -283,9 +333,9 @@ paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         };
         if (!w.done()) look_up(w, z);
         while (ok && !w.done()) {
-            const int ks = li & 1;
+            const int ks = li % C::kPairs;
             const int n_kt = w.two() ? 2 : 1;
-            if (li >= 2 && !(ok = wait(&bars->k_empty[ks], ((li >> 1) - 1) & 1))) break;
+            if (li >= C::kPairs && !(ok = wait(&bars->k_empty[ks], (li / C::kPairs - 1) & 1))) break;
             if (lane == 0) {
                 if (!w.whole()) {
                     PagedPart& p = a.parts[2 * blockIdx.x + (w.first ? 0 : 1)];
@@ -312,24 +362,43 @@ paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             ahead.next(a);
             if (!ahead.done()) look_up(ahead, z_next);
             ++li;
+            w = ahead;
+            z[0] = z_next[0];
+            z[1] = z_next[1];
+        }
+        // never leave with copies in flight
+        for (int i = li > C::kPairs ? li - C::kPairs : 0; i < li; ++i)
+            mbar_wait(&bars->k_full[i % C::kPairs], (i / C::kPairs) & 1, nullptr);
+    } else if (warp == kQWarp) {
+        // ------------------------------------------------ Q and its rows' lse
+        int qc = 0;                 // tiles asked for
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, unsigned parity) -> bool {
+            const int got = lane != 0 || mbar_wait(bar, parity, abort_flag);
+            return __shfl_sync(0xffffffffu, got, 0) != 0;
+        };
+        // the lane's four rows of a tile: token, and place in [token, head] lse
+        int tok[4], at[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int row = 32 * e + (int)lane;
+            tok[e] = row < tt * G ? row / G : 1 << 30;
+            at[e] = row / G * a.H + row % G;
+        }
+        for (; ok && !w.done(); w.next(a)) {
             const int f = first_tile(w.sq, tt, w.i);
             for (int u = w.u0; ok && u < w.u1; ++u) {
                 const int s = qc % C::kQStages;
                 const int tok0 = (f + u) * tt;
-                // the rows' lse, loaded while the stage drains
-                float ls[4];
+                const float* rows = a.lse + (size_t)(w.sq.q0 + tok0) * a.H + w.h * G;
+                float ls[4];        // loaded while the stage drains
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int row = 32 * e + (int)lane;
-                    const int tok = tok0 + row / G;
-                    ls[e] = row < tt * G && tok < w.sq.n
-                                ? a.lse[(size_t)(w.sq.q0 + tok) * a.H + w.h * G + row % G] * kLog2e : 0.f;
-                }
+                for (int e = 0; e < 4; ++e) ls[e] = tok[e] < w.sq.n - tok0 ? rows[at[e]] * -kLog2e : 0.f;
                 if (qc >= C::kQStages && !(ok = wait(&bars->q_empty[s], (qc / C::kQStages - 1) & 1))) break;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(&bars->q_full[s], (unsigned)(G * tt * D * 2));
                     for (int x = 0; x < D / 64; ++x)
-                        tma_load_3d(sQ + s * C::kTileBytes + x * C::kBoxBytes, &tm_q, &bars->q_full[s], x * 64, w.h * G,
+                        tma_load_3d(sQ + s * C::kQBytes + x * C::kQBox, &tm_q, &bars->q_full[s], x * 64, w.h * G,
                                     w.sq.q0 + tok0);
                 }
 #pragma unroll
@@ -338,12 +407,7 @@ paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                 if (lane == 0) mbar_arrive(&bars->q_full[s]);
                 ++qc;
             }
-            w = ahead;
-            z[0] = z_next[0];
-            z[1] = z_next[1];
         }
-        // never leave with copies in flight
-        for (int i = li > 2 ? li - 2 : 0; i < li; ++i) mbar_wait(&bars->k_full[i & 1], (i >> 1) & 1, nullptr);
         for (int c = qc > C::kQStages ? qc - C::kQStages : 0; c < qc; ++c)
             mbar_wait(&bars->q_full[c % C::kQStages], (c / C::kQStages) & 1, nullptr);
     } else if (warp == 1) {
@@ -357,9 +421,9 @@ paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             int li = 0, qc = 0;
             int cnt0 = 0, cnt1 = 0;   // units of each key tile: buffer and phase of s_full / s_free
             for (; ok && !w.done(); w.next(a), ++li) {
-                const int ks = li & 1;
+                const int ks = li % C::kPairs;
                 const bool two = w.two();
-                if (!(ok = mbar_wait(&bars->k_full[ks], (li >> 1) & 1, abort_flag))) break;
+                if (!(ok = mbar_wait(&bars->k_full[ks], (li / C::kPairs) & 1, abort_flag))) break;
                 for (int u = w.u0; ok && u < w.u1; ++u, ++qc) {
                     const int s = qc % C::kQStages;
                     if (!(ok = mbar_wait(&bars->q_full[s], (qc / C::kQStages) & 1, abort_flag))) break;
@@ -374,7 +438,7 @@ paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                         for (int kk = 0; kk < D / 16; ++kk)
                             mma_ss_desc(tmem + (unsigned)(t * 256 + buf * 128),
                                         k_lo + (2 * ks + t) * kStep + PageTile<D>::kmajor(kk), PageTile<D>::kHi,
-                                        q_lo + s * kStep + kmajor_step(kk), kDescHiSw128, idesc, kk > 0);
+                                        q_lo + s * (C::kQBytes >> 4) + (kk >> 2) * (C::kQBox >> 4) + (kk & 3) * 2, kDescHiSw128, idesc, kk > 0);
                         mma_commit(&bars->s_full[t][buf]);
                         if (t) ++cnt1; else ++cnt0;
                     }
@@ -387,20 +451,25 @@ paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             mbar_wait(&bars->drain, 0, nullptr);
         }
     } else {
-        // ------------------------------------------------ one thread per key
-        const int t = (warp - 2) >> 2;
+        // ------------------------------------------------ two threads per key
+        const int t = ((warp - 2) >> 2) & 1;               // key tile
+        const int half = (int)(warp - 2) >> 3;             // columns [64 half, 64 half + 64) of every unit
         const unsigned sub = warp & 3;
         const int r = (int)sub * 32 + (int)lane;
-        const unsigned tS = tmem + ((sub * 32u) << 16) + (unsigned)t * 256u;
+        const unsigned tS = tmem + ((sub * 32u) << 16) + (unsigned)(t * 256 + half * 64);
         const float c_log2 = a.scale * kLog2e;
+        // a wait that gives up does so for the whole warp: the code behind it is collective
+        auto wait_all = [&](uint64_t* bar, unsigned parity) -> bool {
+            return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
+        };
         bool ok = true;
         int cnt = 0, qc = 0;
-        for (; ok && !w.done(); w.next(a)) {
+        for (int li = 0; ok && !w.done(); w.next(a), ++li) {
             const int key = (2 * w.i + t) * kTile + r;
             const bool work = t == 0 || w.two();
-            const bool mine = key < w.sq.L;
             const bool whole = w.whole();
             // the slot and its sum so far, loaded while the tiles arrive
+            const bool mine = half == 0 && key < w.sq.L;
             size_t at = 0;
             float old = 0.f;
             if (mine && whole) {
@@ -408,27 +477,28 @@ paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                 old = a.weights[at];
             }
             const int f = first_tile(w.sq, tt, w.i);
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            const int seen = w.sq.L - w.sq.n;
+            float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
             for (int u = w.u0; u < w.u1; ++u, ++qc) {
                 const int s = qc % C::kQStages;
-                if (!(ok = mbar_wait(&bars->q_full[s], (qc / C::kQStages) & 1, abort_flag))) break;
+                if (!(ok = wait_all(&bars->q_full[s], (qc / C::kQStages) & 1))) break;
                 if (!work) {
                     mbar_arrive(&bars->q_empty[s]);
                     continue;
                 }
                 const int buf = cnt & 1;
-                if (!(ok = mbar_wait(&bars->s_full[t][buf], (cnt >> 1) & 1, abort_flag))) break;
+                if (!(ok = wait_all(&bars->s_full[t][buf], (cnt >> 1) & 1))) break;
                 ++cnt;
                 tc_fence_after();
                 const int tok0 = (f + u) * tt;
-                const int rows = min(tt, w.sq.n - tok0) * G;
-                // the first column that sees this key, and whether some lane of the warp masks any
-                const int first = max(0, key - (w.sq.L - w.sq.n) - tok0) * G;
-                const bool masked = (key - (int)lane + 31 - (w.sq.L - w.sq.n) - tok0) > 0;
-                const float* ls = sLse + s * kTile;
-#pragma unroll
-                for (int c0 = 0; c0 < kTile; c0 += 32) {
-                    if (c0 >= rows) break;
+                // this half's rows, the first one that sees this key, and whether
+                // some lane of the warp masks any
+                const int rows = min(tt, w.sq.n - tok0) * G - half * 64;
+                const int first = max(0, key - seen - tok0) * G - half * 64;
+                const bool masked = key - (int)lane + 31 - seen - tok0 > 0;
+                const float* ls = sLse + s * kTile + half * 64;
+#pragma unroll 1
+                for (int c0 = 0; c0 < min(rows, 64); c0 += 32) {
                     uint32_t x[32];
                     tmem_ld32(tS + buf * 128 + c0, x);
                     tmem_wait_ld();
@@ -436,16 +506,17 @@ paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
 #pragma unroll
                         for (int i = 0; i < 32; i += 4) {
                             const float4 l4 = *reinterpret_cast<const float4*>(ls + c0 + i);
-                            sum[0] += ex2_approx(fmaf(__uint_as_float(x[i]), c_log2, -l4.x));
-                            sum[1] += ex2_approx(fmaf(__uint_as_float(x[i + 1]), c_log2, -l4.y));
-                            sum[2] += ex2_approx(fmaf(__uint_as_float(x[i + 2]), c_log2, -l4.z));
-                            sum[3] += ex2_approx(fmaf(__uint_as_float(x[i + 3]), c_log2, -l4.w));
+                            float p0, p1, p2, p3;
+                            scale_pair(p0, p1, __uint_as_float(x[i]), __uint_as_float(x[i + 1]), c_log2, l4.x, l4.y);
+                            scale_pair(p2, p3, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]), c_log2, l4.z, l4.w);
+                            add_pair(sum[i & 4], sum[(i & 4) + 1], ex2_approx(p0), ex2_approx(p1));
+                            add_pair(sum[(i & 4) + 2], sum[(i & 4) + 3], ex2_approx(p2), ex2_approx(p3));
                         }
                     } else {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
-                            const float p = ex2_approx(fmaf(__uint_as_float(x[i]), c_log2, -ls[c0 + i]));
-                            if (c0 + i >= first && c0 + i < rows) sum[i & 3] += p;
+                            const float p = ex2_approx(fmaf(__uint_as_float(x[i]), c_log2, ls[c0 + i]));
+                            if (c0 + i >= first && c0 + i < rows) sum[i & 7] += p;
                         }
                     }
                 }
@@ -454,11 +525,22 @@ paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                 mbar_arrive(&bars->q_empty[s]);
             }
             if (!ok) break;
-            const float total = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            if (whole) {
-                if (mine) a.weights[at] = old + total;
+            float total = ((sum[0] + sum[1]) + (sum[2] + sum[3])) + ((sum[4] + sum[5]) + (sum[6] + sum[7]));
+            // the two warps of the same keys: the second half's sum comes through shared memory
+            const int pair = t * 4 + (int)sub;
+            if (half == 1) {
+                if (li > 0 && !(ok = wait_all(&bars->sum_free[pair], (li - 1) & 1))) break;
+                sSum[t * kTile + r] = total;
+                mbar_arrive(&bars->sum_full[pair]);
             } else {
-                a.part_sum[(size_t)(2 * blockIdx.x + (w.first ? 0 : 1)) * 2 * kTile + t * kTile + r] = total;
+                if (!(ok = wait_all(&bars->sum_full[pair], li & 1))) break;
+                total += sSum[t * kTile + r];
+                mbar_arrive(&bars->sum_free[pair]);
+                if (whole) {
+                    if (mine) a.weights[at] = old + total;
+                } else {
+                    a.part_sum[(size_t)(2 * blockIdx.x + (w.first ? 0 : 1)) * 2 * kTile + t * kTile + r] = total;
+                }
             }
         }
     }
@@ -494,10 +576,10 @@ __global__ void __launch_bounds__(2 * kTile) weights_merge_kernel(const PagedWei
     if (key < sq.L) a.weights[weight_at(a.s, a.Hkv, p.b, p.h, key)] += sum;
 }
 
-template <int D>
+template <int D, bool FEW>
 cudaError_t launch_d(const PagedWeightsTcArgs& a, int sm_count, cudaStream_t stream) {
-    using C = Cfg<D>;
-    auto kern = paged_weights_tc_kernel<D>;
+    using C = Cfg<D, FEW>;
+    auto kern = paged_weights_tc_kernel<D, FEW>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];
@@ -521,7 +603,9 @@ cudaError_t launch_d(const PagedWeightsTcArgs& a, int sm_count, cudaStream_t str
 }  // namespace
 
 cudaError_t launch_paged_weights_tc(const PagedWeightsTcArgs& a, int sm_count, cudaStream_t stream) {
-    return a.D == 64 ? launch_d<64>(a, sm_count, stream) : launch_d<128>(a, sm_count, stream);
+    const bool few = a.tt * (a.H / a.Hkv) <= kFewRows;
+    if (a.D == 64) return few ? launch_d<64, true>(a, sm_count, stream) : launch_d<64, false>(a, sm_count, stream);
+    return few ? launch_d<128, true>(a, sm_count, stream) : launch_d<128, false>(a, sm_count, stream);
 }
 
 }  // namespace mea
