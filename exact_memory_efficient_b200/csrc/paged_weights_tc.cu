@@ -15,10 +15,10 @@
 // workspace slot, to be added in order by weights_merge_kernel; without it (one
 // query tile per item: decode) a CTA takes the items that begin in its share.
 //
-// Roles (608 threads): warp 0 TMA producer of K (a pair of tiles per item), warp
-// 18 of Q (a tile per unit, with its rows' lse), warp 1 MMA issuer; of the two key
-// tiles each has eight warps, four for the first 64 columns of every unit and
-// four for the others, whose sums are added at the item's end.
+// Roles: warp 0 TMA producer of K (a pair of tiles per item), the last warp of Q (a
+// tile per unit, with its rows' lse), warp 1 MMA issuer; of the two key tiles each
+// has eight warps, four for the first 64 columns of every unit and four for the
+// others, whose sums are added at the item's end (four warps with few rows).
 // TMEM: two score buffers of 128 columns per key tile.
 //
 // Bound: decode reads K once (HBM); with many rows one exponential per score
@@ -37,8 +37,6 @@ namespace mea {
 namespace {
 
 constexpr int kTile = 128;
-constexpr int kThreads = 608;         // 19 warps
-constexpr int kQWarp = 18;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // FEW: at most kFewRows rows per query tile (decode).  Q then takes 2 KB per 64
@@ -46,9 +44,13 @@ constexpr float kLog2e = 1.4426950408889634f;
 // D = 128 (six at D = 64), since decode is bound by the bytes in flight.
 constexpr int kFewRows = 16;
 constexpr int kMaxPairs = 6;
+constexpr int kMaxThreads = 608;
 
 template <int D, bool FEW>
 struct Cfg {
+    static constexpr int kHalves = FEW ? 1 : 2;                      // warps per 32 keys
+    static constexpr int kQWarp = 2 + 8 * kHalves;
+    static constexpr int kThreads = 32 * (kQWarp + 1);
     static constexpr int kTileBytes = kTile * D * 2;
     static constexpr int kQBox = FEW ? kFewRows * 128 : 128 * 128;   // 64 head dims of a query tile
     static constexpr int kQBytes = D / 64 * kQBox;
@@ -75,7 +77,7 @@ struct Barriers {
         int b, h, i, u0;
         long long units;
     } share;
-    long long warp_sum[kThreads / 32];
+    long long warp_sum[kMaxThreads / 32];
 };
 
 __device__ __forceinline__ int q_tiles(const Seq& sq, int tt) { return (sq.n + tt - 1) / tt; }
@@ -141,7 +143,9 @@ struct Walk {
     __device__ __forceinline__ bool two() const { return i * 2 * kTile + kTile < sq.L; }   // the second key tile has keys
 };
 
+template <int THREADS>
 __device__ __forceinline__ void find_share(const PagedWeightsTcArgs& a, Barriers* bars) {
+    constexpr int kThreads = THREADS;
     const int tid = (int)threadIdx.x;
     const unsigned lane = lane_id(), warp = warp_id();
     Seq sq;
@@ -245,7 +249,7 @@ __device__ __forceinline__ size_t weight_at(const PagedBatch& s, int Hkv, int b,
 }
 
 template <int D, bool FEW>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<D, FEW>::kThreads, 1)
 paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const PagedWeightsTcArgs a) {
     using C = Cfg<D, FEW>;
@@ -270,12 +274,12 @@ paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         for (int i = 0; i < 2; ++i) {
             for (int j = 0; j < 2; ++j) {
                 mbar_init(&bars->s_full[i][j], 1);
-                mbar_init(&bars->s_free[i][j], 256);
+                mbar_init(&bars->s_free[i][j], 128 * C::kHalves);
             }
         }
         for (int i = 0; i < C::kQStages; ++i) {
             mbar_init(&bars->q_full[i], 2);    // the copies, and the rows' lse
-            mbar_init(&bars->q_empty[i], 513);   // both MMAs, and the readers of lse
+            mbar_init(&bars->q_empty[i], 1 + 256 * C::kHalves);   // both MMAs, and the readers of lse
         }
         for (int i = 0; i < 8; ++i) {
             mbar_init(&bars->sum_full[i], 32);
@@ -300,7 +304,7 @@ paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     volatile int* abort_flag = &bars->abort_flag;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    find_share(a, bars);
+    find_share<C::kThreads>(a, bars);
 
     Walk w;
     w.begin(a, bars);
@@ -369,7 +373,7 @@ paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         // never leave with copies in flight
         for (int i = li > C::kPairs ? li - C::kPairs : 0; i < li; ++i)
             mbar_wait(&bars->k_full[i % C::kPairs], (i / C::kPairs) & 1, nullptr);
-    } else if (warp == kQWarp) {
+    } else if (warp == C::kQWarp) {
         // ------------------------------------------------ Q and its rows' lse
         int qc = 0;                 // tiles asked for
         bool ok = true;
@@ -451,7 +455,7 @@ paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             mbar_wait(&bars->drain, 0, nullptr);
         }
     } else {
-        // ------------------------------------------------ two threads per key
+        // ------------------------------------------------ one or two threads per key
         const int t = ((warp - 2) >> 2) & 1;               // key tile
         const int half = (int)(warp - 2) >> 3;             // columns [64 half, 64 half + 64) of every unit
         const unsigned sub = warp & 3;
@@ -468,14 +472,9 @@ paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             const int key = (2 * w.i + t) * kTile + r;
             const bool work = t == 0 || w.two();
             const bool whole = w.whole();
-            // the slot and its sum so far, loaded while the tiles arrive
+            // the key's page, looked up while the tiles arrive and not used before the end
             const bool mine = half == 0 && key < w.sq.L;
-            size_t at = 0;
-            float old = 0.f;
-            if (mine && whole) {
-                at = weight_at(a.s, a.Hkv, w.b, w.h, key);
-                old = a.weights[at];
-            }
+            const int page = mine && whole ? load_page(a.s, w.b, key >> a.s.page_shift) : 0;
             const int f = first_tile(w.sq, tt, w.i);
             const int seen = w.sq.L - w.sq.n;
             float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -497,6 +496,17 @@ paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                 const int first = max(0, key - seen - tok0) * G - half * 64;
                 const bool masked = key - (int)lane + 31 - seen - tok0 > 0;
                 const float* ls = sLse + s * kTile + half * 64;
+                if constexpr (FEW) {
+                    uint32_t x[16];
+                    tmem_ld16(tS + buf * 128, x);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < kFewRows; ++i) {
+                        if (i >= rows) break;
+                        const float p = ex2_approx(fmaf(__uint_as_float(x[i]), c_log2, ls[i]));
+                        if (i >= first) sum[i & 7] += p;
+                    }
+                } else {
 #pragma unroll 1
                 for (int c0 = 0; c0 < min(rows, 64); c0 += 32) {
                     uint32_t x[32];
@@ -520,27 +530,33 @@ paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                         }
                     }
                 }
+                }
                 tc_fence_before();
                 mbar_arrive(&bars->s_free[t][buf]);
                 mbar_arrive(&bars->q_empty[s]);
             }
             if (!ok) break;
             float total = ((sum[0] + sum[1]) + (sum[2] + sum[3])) + ((sum[4] + sum[5]) + (sum[6] + sum[7]));
-            // the two warps of the same keys: the second half's sum comes through shared memory
-            const int pair = t * 4 + (int)sub;
-            if (half == 1) {
-                if (li > 0 && !(ok = wait_all(&bars->sum_free[pair], (li - 1) & 1))) break;
-                sSum[t * kTile + r] = total;
-                mbar_arrive(&bars->sum_full[pair]);
-            } else {
+            if constexpr (C::kHalves == 2) {
+                // the two warps of the same keys: the second half's sum comes through shared memory
+                const int pair = t * 4 + (int)sub;
+                if (half == 1) {
+                    if (li > 0 && !(ok = wait_all(&bars->sum_free[pair], (li - 1) & 1))) break;
+                    sSum[t * kTile + r] = total;
+                    mbar_arrive(&bars->sum_full[pair]);
+                    continue;
+                }
                 if (!(ok = wait_all(&bars->sum_full[pair], li & 1))) break;
                 total += sSum[t * kTile + r];
                 mbar_arrive(&bars->sum_free[pair]);
-                if (whole) {
-                    if (mine) a.weights[at] = old + total;
-                } else {
-                    a.part_sum[(size_t)(2 * blockIdx.x + (w.first ? 0 : 1)) * 2 * kTile + t * kTile + r] = total;
-                }
+            }
+            if (!whole) {
+                a.part_sum[(size_t)(2 * blockIdx.x + (w.first ? 0 : 1)) * 2 * kTile + t * kTile + r] = total;
+            } else if (mine) {
+                // one addition per slot and call, so its order cannot matter: a
+                // reduction that nothing waits for (old + total, rounded once)
+                atomicAdd(&a.weights[(((size_t)page * a.Hkv + w.h) << a.s.page_shift) + (key & ((1 << a.s.page_shift) - 1))],
+                          total);
             }
         }
     }
@@ -587,7 +603,7 @@ cudaError_t launch_d(const PagedWeightsTcArgs& a, int sm_count, cudaStream_t str
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)sm_count);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = C::kSmemBytes;
     cfg.stream = stream;
     cfg.attrs = attr;
