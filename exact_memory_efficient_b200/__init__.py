@@ -23,7 +23,6 @@ Serving over a cache in pages (packed tokens; include/mea_attn.h has the layout)
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -543,11 +542,25 @@ def _raw_stream(device: int) -> int:
     return int(get(device)) if get is not None else int(torch.cuda.current_stream(device).cuda_stream)
 
 
+def _dense(shape):
+    """Strides of a contiguous tensor."""
+    n = len(shape)
+    if n == 1:
+        return (1,)
+    if n == 2:
+        return (shape[1], 1)
+    if n == 3:
+        return (shape[1] * shape[2], shape[2], 1)
+    return (shape[1] * shape[2] * shape[3], shape[2] * shape[3], shape[3], 1)
+
+
 def _empty(stream, like, *shapes):
     """Tensors of the (shape, dtype) pairs on ``like``'s device, allocated on ``stream`` where one is
     given, so that the allocator does not hand their memory on while the call may still run."""
     if stream is None:
-        return [like.new_empty(shape, dtype=dtype) if shape is not None else None for shape, dtype in shapes]
+        dev, make = like.device, torch.empty_strided     # the cheapest of torch's allocations
+        return [make(shape, _dense(shape), dtype=dtype, device=dev) if shape is not None else None
+                for shape, dtype in shapes]
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(_stream_handle(stream), device=like.device)
     with torch.cuda.stream(stream):
@@ -567,7 +580,8 @@ def mea_rope(x, y, positions, freq, layout: int = MEA_ROPE_HALF, mscale: float =
         _bad("mea_rope", "positions must be [N] or [B, N]")
     dev = _same_device("mea_rope", x, (("x", x, x.dtype), ("y", y, x.dtype), ("positions", positions, torch.int32),
                                        ("freq", freq, torch.float64)))
-    _launch("mea_rope", load_library().mea_rope, dev, stream, _ptr(x), _ptr(y), _ptr(positions), _ptr(freq), B, H,
+    _launch("mea_rope", load_library().mea_rope, dev, stream, x.data_ptr(), y.data_ptr(), positions.data_ptr(),
+            freq.data_ptr(), B, H,
             N, D, 2 * freq.shape[0], int(positions.dim() == 2), int(layout), float(mscale), int(bool(inverse)),
             _dtype_code(x))
 
@@ -608,8 +622,9 @@ def mea_paged_append(q, q_out, k, v, k_cache, v_cache, weights, cu_q, kv_len, pa
                         ("freq", freq, torch.float64), ("q_out", q_out, dt)))
     if v.get_device() != dev or (q is not None and q.get_device() != dev):
         _bad(w, "q, k and v must be on one device")
-    _launch(w, load_library().mea_paged_append, dev, stream, _ptr(q), _ptr(q_out), _ptr(k), _ptr(v),
-            _ptr(k_cache), _ptr(v_cache), _ptr(weights), _ptr(cu_q), _ptr(kv_len), _ptr(page_table), _ptr(positions),
+    _launch(w, load_library().mea_paged_append, dev, stream, _ptr(q), _ptr(q_out), k.data_ptr(), v.data_ptr(),
+            k_cache.data_ptr(), v_cache.data_ptr(), _ptr(weights), cu_q.data_ptr(), kv_len.data_ptr(),
+            page_table.data_ptr(), _ptr(positions),
             _ptr(freq), T, B, H, Hkv, D, qs, ks, vs, pages, page, max_pages, 0 if freq is None else 2 * freq.shape[0],
             int(layout), float(mscale), _dtype_code(k_cache))
 
@@ -645,11 +660,6 @@ def mea_attn_paged_weights_workspace_size(T: int, B: int, H: int, H_kv: int, D: 
                             (T, B, H, H_kv, D, max_q, max_kv), dtype)
 
 
-def _on(t):
-    """Context with ``t``'s device current (nothing to do where it is)."""
-    return contextlib.nullcontext() if t.get_device() == torch.cuda.current_device() else torch.cuda.device(t.device)
-
-
 def _workspace_bytes(where: str, workspace, device: int) -> int:
     if workspace is None:
         return 0
@@ -674,26 +684,36 @@ def mea_attn_paged(q, k_cache, v_cache, o, lse, cu_q, kv_len, page_table, max_q:
                         ("cu_q", cu_q, torch.int32), ("kv_len", kv_len, torch.int32),
                         ("page_table", page_table, torch.int32)))
     ws_bytes = _workspace_bytes(w, workspace, dev)
-    _launch(w, load_library().mea_attn_paged, dev, stream, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(o),
-            _ptr(lse), _ptr(cu_q), _ptr(kv_len), _ptr(page_table), T, B, H, Hkv, D, qs, pages, page, max_pages,
+    _launch(w, load_library().mea_attn_paged, dev, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            o.data_ptr(),
+            lse.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), T, B, H, Hkv, D, qs, pages,
+            page, max_pages,
             int(max_q), int(max_kv), float(scale), _dtype_code(q), _ptr(workspace), ws_bytes)
+
+
+def _paged_call(where: str, size, q, k_cache, kv_len, max_q: int, max_kv: int, scale):
+    """T, H, D, workspace bytes and scale of a call that allocates for itself."""
+    if q.dim() != 3 or k_cache.dim() != 4 or kv_len.dim() != 1:
+        _bad(where, "q must be [T, H, D], k_cache [pages, H_kv, page_size, D] and kv_len [B]")
+    if not q.is_cuda:
+        _bad(where, "CUDA tensors")
+    T, H, D = q.shape
+    sizes = (T, kv_len.shape[0], H, k_cache.shape[1], D, max_q, max_kv, q.dtype)
+    if q.get_device() == torch.cuda.current_device():
+        n = size(*sizes)
+    else:
+        with torch.cuda.device(q.device):
+            n = size(*sizes)
+    return T, H, D, n, 1.0 / math.sqrt(D) if scale is None else scale
 
 
 def attention_paged(q, k_cache, v_cache, cu_q, kv_len, page_table, max_q: int, max_kv: int,
                     scale: float | None = None, stream=None):
     """Allocate (o, lse) and the workspace with torch and run ``mea_attn_paged``.  Rows outside every
     sequence are not written."""
-    _pages("attention_paged", k_cache)
-    if q.dim() != 3:
-        _bad("attention_paged", "q must be [T, H, D]")
-    if not q.is_cuda:
-        _bad("attention_paged", "CUDA tensors")
-    if scale is None:
-        scale = 1.0 / math.sqrt(q.shape[-1])
-    T, H, D = q.shape
-    with _on(q):
-        n = mea_attn_paged_workspace_size(T, kv_len.shape[0], H, k_cache.shape[1], D, max_q, max_kv, q.dtype)
-    o, lse, ws = _empty(stream, q, (q.shape, q.dtype), ((T, H), torch.float32), ((n,) if n else None, torch.uint8))
+    T, H, D, n, scale = _paged_call("attention_paged", mea_attn_paged_workspace_size, q, k_cache, kv_len, max_q, max_kv,
+                                    scale)
+    o, lse, ws = _empty(stream, q, ((T, H, D), q.dtype), ((T, H), torch.float32), ((n,) if n else None, torch.uint8))
     mea_attn_paged(q, k_cache, v_cache, o, lse, cu_q, kv_len, page_table, max_q, max_kv, scale, ws, stream)
     return o, lse
 
@@ -713,8 +733,9 @@ def mea_attn_paged_weights(q, lse, k_cache, weights, cu_q, kv_len, page_table, m
     dev = _same_device(w, q, (("k_cache", k_cache, k_cache.dtype), ("weights", weights, torch.float32),
                         ("lse", lse, torch.float32), ("cu_q", cu_q, torch.int32), ("kv_len", kv_len, torch.int32),
                         ("page_table", page_table, torch.int32)))
-    _launch(w, load_library().mea_attn_paged_weights, dev, stream, _ptr(q), _ptr(lse), _ptr(k_cache),
-            _ptr(weights), _ptr(cu_q), _ptr(kv_len), _ptr(page_table), T, B, H, Hkv, D, qs, pages, page, max_pages,
+    _launch(w, load_library().mea_attn_paged_weights, dev, stream, q.data_ptr(), lse.data_ptr(), k_cache.data_ptr(),
+            weights.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), T, B, H, Hkv, D, qs,
+            pages, page, max_pages,
             int(max_q), int(max_kv), float(scale), _dtype_code(q), _ptr(workspace),
             _workspace_bytes(w, workspace, dev))
 
@@ -722,17 +743,10 @@ def mea_attn_paged_weights(q, lse, k_cache, weights, cu_q, kv_len, page_table, m
 def attention_paged_weights(q, lse, k_cache, weights, cu_q, kv_len, page_table, max_q: int, max_kv: int,
                             scale: float | None = None, stream=None) -> None:
     """Allocate the workspace with torch and run ``mea_attn_paged_weights``."""
-    _pages("attention_paged_weights", k_cache, None, weights)
-    if q.dim() != 3:
-        _bad("attention_paged_weights", "q must be [T, H, D]")
-    if not q.is_cuda:
-        _bad("attention_paged_weights", "CUDA tensors")
-    T, H, D = q.shape
-    with _on(q):
-        n = mea_attn_paged_weights_workspace_size(T, kv_len.shape[0], H, k_cache.shape[1], D, max_q, max_kv, q.dtype)
+    _, _, _, n, scale = _paged_call("attention_paged_weights", mea_attn_paged_weights_workspace_size, q, k_cache, kv_len,
+                                    max_q, max_kv, scale)
     ws, = _empty(stream, q, ((n,) if n else None, torch.uint8))
-    mea_attn_paged_weights(q, lse, k_cache, weights, cu_q, kv_len, page_table, max_q, max_kv,
-                           1.0 / math.sqrt(D) if scale is None else scale, ws, stream)
+    mea_attn_paged_weights(q, lse, k_cache, weights, cu_q, kv_len, page_table, max_q, max_kv, scale, ws, stream)
 
 
 def mea_paged_evict(k_cache, v_cache, weights, page_table, kv_len, dst_table, kv_len_out, keep_idx, n_recent: int,
@@ -753,8 +767,9 @@ def mea_paged_evict(k_cache, v_cache, weights, page_table, kv_len, dst_table, kv
                               ("weights", weights, torch.float32), ("page_table", page_table, i32),
                               ("kv_len", kv_len, i32), ("dst_table", dst_table, i32), ("keep_idx", keep_idx, i32),
                               ("kv_len_out", kv_len_out, i32)))
-    _launch(w, load_library().mea_paged_evict, dev, stream, _ptr(k_cache), _ptr(v_cache), _ptr(weights),
-            _ptr(page_table), _ptr(kv_len), _ptr(dst_table), _ptr(kv_len_out), _ptr(keep_idx), B, Hkv, D, pages, page,
+    _launch(w, load_library().mea_paged_evict, dev, stream, k_cache.data_ptr(), v_cache.data_ptr(), weights.data_ptr(),
+            page_table.data_ptr(), kv_len.data_ptr(), dst_table.data_ptr(), _ptr(kv_len_out), keep_idx.data_ptr(), B,
+            Hkv, D, pages, page,
             max_pages, dst_table.shape[1], keep_idx.shape[2], int(n_recent), _dtype_code(k_cache))
 
 
