@@ -120,7 +120,9 @@ cudaError_t launch_t(const PagedWeightsArgs& a, cudaStream_t stream) {
     const size_t smem = (size_t)a.D * (kKeys + kPad + kRows + kPad) * sizeof(float);
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    const long long tiles = ((long long)a.max_kv + kKeys - 1) / kKeys;
+    // max_kv is only a bound on what is usual: a CTA walks on from tile to tile
+    const long long cap = (long long)a.s.max_pages << a.s.page_shift;
+    const long long tiles = ((a.max_kv < cap ? a.max_kv : cap) + kKeys - 1) / kKeys;
     const dim3 grid((unsigned)(tiles < 1 ? 1 : tiles), (unsigned)a.Hkv, (unsigned)a.s.B);
     kern<<<grid, kThreads, smem, stream>>>(a);
     return cudaGetLastError();

@@ -221,3 +221,84 @@ def test_bad_tables_are_reported():
             st = m.mea_last_device_error()
             assert st == m.MEA_ERR_PAGE or ("cu" in x and st == m.MEA_OK)
         check(bt, run(bt))
+
+
+def test_many_sequences():
+    """More sequences than a CTA has threads, most of them short, some without new tokens."""
+    g = torch.Generator().manual_seed(14)
+    lens = torch.randint(1, 70, (900,), generator=g).tolist()
+    lens[417] = 2000
+    counts = [min(n, int(c)) for n, c in zip(lens, torch.randint(0, 4, (900,), generator=g))]
+    counts[417] = 300
+    bt = Batch(counts, lens, 4, 2, 64, 16, BF, seed=15)
+    check(bt, run(bt))
+    bt = Batch([1] * 900, lens, 4, 2, 64, 16, BF, seed=16)
+    check(bt, run(bt))
+
+
+@pytest.mark.parametrize("dtype,G,D", [(BF, 128, 64), (BF, 130, 64), (BF, 43, 128), (F32, 20, 32)])
+def test_large_groups(dtype, G, D):
+    """Groups up to a whole query tile, and beyond one (the CUDA-core kernel takes those)."""
+    bt = Batch([1, 3], [200, 131], 2 * G, 2, D, 32, dtype, seed=17)
+    check(bt, run(bt))
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.125, -3.0])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_scale_of_zero_and_below(dtype, scale):
+    for counts, lens in (([1, 1], [300, 45]), ([140, 3], [150, 45])):
+        bt = Batch(counts, lens, 4, 2, 64, 16, dtype, seed=18)
+        bt.scale = scale
+        check(bt, run(bt))
+
+
+def test_nothing_to_do():
+    bt = Batch([2], [20], 4, 2, 64, 16, BF)
+    q, kc, vc, cu, kv, tab = bt.gpu("q", "k_cache", "v_cache", "cu", "kv_len", "table")
+    o, lse = m.attention_paged(q[:0], kc, vc, cu * 0, kv, tab, 0, 20)
+    assert o.shape == (0, 4, 64) and lse.shape == (0, 4)
+    o, lse = m.attention_paged(q, kc, vc, cu[:1].contiguous(), kv[:0], tab[:0], 0, 0)     # no sequences
+    assert o.shape == q.shape
+
+
+def test_one_row_with_any_stride():
+    """A single row's token stride means nothing."""
+    bt = Batch([1], [77], 4, 2, 64, 16, BF, seed=19)
+    q = torch.as_strided(bt.q.cuda(), (1, 4, 64), (1, 64, 1))
+    check(bt, run(bt, q=q))
+
+
+@pytest.mark.parametrize("dtype,D", [(BF, 128), (F32, 64)])
+def test_offsets_beyond_32_bits(dtype, D):
+    """A cache of more than 2^32 elements whose sequences lie at its end: append, attention, weights, eviction."""
+    counts, lens, H, Hkv, page = [1, 70], [300, 90], 4, 2, 256
+    bt = Batch(counts, lens, H, Hkv, D, page, dtype, seed=20, spare=4)
+    pages = (1 << 32) // (Hkv * page * D) + 40
+    shift = pages - bt.pages
+    big = []
+    for t in (bt.k_cache, bt.v_cache):
+        x = torch.empty(pages, Hkv, page, D, dtype=dtype, device="cuda")
+        x[shift:] = t.cuda()
+        big.append(x)
+    assert big[0].numel() > 1 << 32
+    w = torch.zeros(pages, Hkv, page, device="cuda")
+    w[shift:] = bt.weights.cuda()
+    table = torch.where(bt.table >= 0, bt.table + shift, bt.table).int()
+    q, k, v, cu, kv = bt.gpu("q", "k", "v", "cu", "kv_len")
+    m.paged_append(None, k, v, *big, w, cu, kv, table.cuda())
+    o, lse = m.attention_paged(q, *big, cu, kv, table.cuda(), 70, 300, bt.scale)
+    m.attention_paged_weights(q, lse, big[0], w, cu, kv, table.cuda(), 70, 300, bt.scale)
+    _, kc, vc, wa = paged.append(None, *bt.np("k", "v", "k_cache", "v_cache", "weights"), bt.cu.numpy(),
+                                 bt.kv_len.numpy(), bt.table.numpy())
+    bt.k_cache, bt.v_cache = torch.from_numpy(kc).to(dtype), torch.from_numpy(vc).to(dtype)
+    check(bt, (o, lse))
+    want = paged.paged_weights(bt.np("q")[0], f64(lse), kc, wa, bt.cu.numpy(), bt.kv_len.numpy(), bt.table.numpy(),
+                               bt.scale)
+    assert np.abs(f64(w[shift:]) - want).max() < 1e-3
+    before = [x[shift:].cpu().float().numpy() for x in (*big, w)]
+    kept, n = m.paged_evict(*big, w, table.cuda(), kv, table.cuda(), 64, 16)
+    ref = paged.evict(*before, bt.table.numpy(), bt.kv_len.numpy(), bt.table.numpy(), 64, 16)
+    assert np.array_equal(kept.cpu().numpy(), ref[3]) and n.tolist() == [64, 64]
+    for x, r in zip((*big, w), ref):
+        assert np.array_equal(x[shift:].cpu().float().numpy(), r)
+    assert m.mea_last_device_error() == m.MEA_OK

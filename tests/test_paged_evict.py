@@ -131,3 +131,11 @@ def test_evict_bad_tables_are_reported():
         assert m.mea_last_device_error() == m.MEA_ERR_PAGE
     m.paged_evict(kc, vc, w, tab, kv, dst, 100, 10)
     assert m.mea_last_device_error() == m.MEA_OK
+
+
+def test_evict_many_sequences():
+    g = torch.Generator().manual_seed(3)
+    lens = torch.randint(0, 120, (700,), generator=g).tolist()
+    bt = Batch([0] * 700, lens, 2, 2, 64, 16, BF, seed=10, spare=3000)
+    check(bt, 40, 8)
+    check(bt, 40, 8, in_place=True)

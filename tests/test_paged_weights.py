@@ -110,3 +110,44 @@ def test_graph_replay_and_bad_tables():
         call(**x)
         st = m.mea_last_device_error()
         assert st == m.MEA_ERR_PAGE or ("cu" in x and st == m.MEA_OK)
+
+
+def test_many_sequences():
+    g = torch.Generator().manual_seed(14)
+    lens = torch.randint(1, 70, (900,), generator=g).tolist()
+    lens[417] = 2000
+    counts = [min(n, int(c)) for n, c in zip(lens, torch.randint(0, 4, (900,), generator=g))]
+    counts[417] = 300
+    for c in (counts, [1] * 900):
+        bt = Batch(c, lens, 4, 2, 64, 16, BF, seed=15)
+        lse = exact_lse(bt)
+        check(bt, lse, run(bt, lse))
+
+
+@pytest.mark.parametrize("dtype,G,D", [(BF, 128, 64), (BF, 130, 64), (BF, 43, 128), (F32, 20, 32)])
+def test_large_groups(dtype, G, D):
+    bt = Batch([1, 3], [200, 131], 2 * G, 2, D, 32, dtype, seed=17)
+    lse = exact_lse(bt)
+    check(bt, lse, run(bt, lse))
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.125])
+def test_scale_of_zero_and_below(scale):
+    for counts, lens in (([1, 1], [300, 45]), ([140, 3], [150, 45])):
+        bt = Batch(counts, lens, 4, 2, 64, 16, BF, seed=18)
+        bt.scale = scale
+        lse = exact_lse(bt)
+        got = run(bt, lse)
+        q, kc, w = bt.np("q", "k_cache", "weights")
+        want = paged.paged_weights(q, f64(lse), kc, w, bt.cu.numpy(), bt.kv_len.numpy(), bt.table.numpy(), scale)
+        bt.scale = abs(scale)      # the bound takes magnitudes, against the exact lse of either sign
+        tol = weight_bound(bt, q if scale >= 0 else -q, f64(lse), want)
+        assert (np.abs(f64(got) - want) <= tol).all()
+
+
+def test_bits_do_not_depend_on_the_run():
+    bt = Batch([900, 1], [1500, 3000], 8, 2, 128, 64, BF, seed=19)
+    lse = torch.zeros(bt.T, 8)
+    a = run(bt, lse)
+    for _ in range(3):
+        assert torch.equal(a, run(bt, lse))
