@@ -34,6 +34,14 @@
 // Slot t holds query tile t of an item and the key tiles that tile sees; when
 // the item has one query tile both slots run it over alternate key tiles and
 // fold their summaries at the end.
+// Bound: with many rows each slot's chain softmax (2,000 cycles: 128 exponentials
+// per row at 16 per clock and SM, and their issue) -> P V -> next S, about 3,550
+// cycles per key tile of an item against 2,048 of MMAs, at the clock that the 1 kW
+// power limit leaves (1.5-1.8 GHz): 2048 tokens over 16384 keys of 16 heads
+// (D = 128) take 263 us, 980 TFLOP/s.  A slot that waits for the other's softmax
+// before its first S, or before every S, is not faster (264 and 298 us).  With few
+// rows HBM: 37 sequences of 4096 keys, 16 over 4 heads, 56 us, 5.5 TB/s.
+//
 // S is masked per row (keys past the row's token).  The values behind a
 // sequence's last key in its last page may be anything, and 0 x NaN is NaN, so
 // the first slot that uses such a V tile overwrites those rows with zeros.
@@ -121,8 +129,11 @@ __device__ __forceinline__ int tiles_of(const Seq& sq, int tt, int i) {
     return max(1, (keys_seen(sq, (i + 1) * 2 * tt) + kTile - 1) / kTile);
 }
 
-// Position in the list of items; walks on item by item.  A key tile costs 1, and
-// so does an item's end (its epilogue takes about as long as a key tile).
+// Position in the list of items; walks on item by item.  A key tile costs 1, an
+// item's end kEndCost: an epilogue takes about 4 us, a key tile 1.9 (1 to 4 measure
+// within 2% of one another; 6 is slower for a ragged decode).
+constexpr int kEndCost = 2;
+
 struct Walk {
     Seq sq;
     int b, h, i, items;
@@ -142,14 +153,14 @@ struct Walk {
         items = items_of(sq, tt);
         n_kv = tiles_of(sq, tt, i);
         t1 = (int)min((long long)n_kv, t0 + left);
-        if (t0 == n_kv) {   // nothing but the end of an item, which the CTA in front has taken
+        if (t0 >= n_kv) {   // nothing but the end of an item, which the CTA in front has taken
             next(s, Hkv, tt);
             first = true;
         }
     }
     __device__ __forceinline__ bool done() const { return left <= 0; }
     __device__ __forceinline__ void next(const PagedBatch& s, int Hkv, int tt) {
-        left -= n_kv + 1 - t0;
+        left -= n_kv + kEndCost - t0;
         first = false;
         if (left <= 0) return;
         if (++i == items) {
@@ -189,7 +200,7 @@ __device__ __forceinline__ void find_share(const PagedTcArgs& a, Barriers* bars)
         sq = load_seq(a.s, b);
         const int items = items_of(sq, a.tt);
         long long sum = 0;
-        for (int i = 0; i < items; ++i) sum += tiles_of(sq, a.tt, i) + 1;
+        for (int i = 0; i < items; ++i) sum += tiles_of(sq, a.tt, i) + kEndCost;
         return sum * a.Hkv;
     };
     // inclusive scan over the block's threads; returns the sum in front of this thread, *all the block's
@@ -234,7 +245,7 @@ __device__ __forceinline__ void find_share(const PagedTcArgs& a, Barriers* bars)
         x -= at.h * per_head;
         int i = 0;
         for (; i + 1 < items; ++i) {
-            const int n = tiles_of(sq, a.tt, i) + 1;
+            const int n = tiles_of(sq, a.tt, i) + kEndCost;
             if (x < n) break;
             x -= n;
         }
@@ -444,11 +455,6 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     it.part = w.whole() ? -1 : 2 * (int)blockIdx.x + (w.first ? 0 : 1);
                     mbar_arrive(&bars->item[li & 3]);
                 }
-                // The slots keep the distance in time at which an item begins: half
-                // a softmax apart each has the exponential unit to itself while
-                // the other's MMAs run.  With both first S issued together the
-                // two softmaxes overlap and a key tile takes 2.2-2.4 us instead of
-                // 1.9 (D = 128).
                 // A slot's first P V overwrites its O.  Its own epilogue of the
                 // item before is over when its softmax hands over P; after a
                 // single item the other slot's epilogue has read it as well.
@@ -463,7 +469,6 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     int v_stage0 = 0, v_stage1 = 0;
                     for (int t = 0; ok && t < 2 && t < n1; ++t) {
                         if (!(ok = next_tile(k_off, k_stage))) break;
-                        if (t == 1 && !FEW && !(ok = mbar_wait(&bars->p_half[0], cnt0 & 1, abort_flag))) break;
                         tc_fence_after();
                         issue_s(t ? tS1 : tS0, q_lo0, k_off);
                         mma_commit(&bars->s_full[t]);
@@ -493,8 +498,6 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     if (n0 > 0) {
                         issue_s(tS0, q_lo0, k_off);
                         mma_commit(&bars->s_full[0]);
-                        // slot 1 begins when slot 0's first softmax is half done (below)
-                        if (!(ok = mbar_wait(&bars->p_half[0], cnt0 & 1, abort_flag))) break;
                     }
                     issue_s(tS1, q_lo1, k_off);
                     mma_commit(&bars->s_full[1]);
