@@ -98,4 +98,53 @@ __device__ __forceinline__ int find_row(const PagedBatch& s, int t) {
     return lo;
 }
 
+// The costs of all sequences as one line: calls locate(b, before, cost, W) for
+// every b, with the sum of the costs in front of b and of all.  All THREADS
+// threads of the block call it; a thread's cost(b) and locate(b, ...) calls
+// follow one another, so that cost() may leave what locate() needs.
+template <int THREADS, typename Cost, typename Locate>
+__device__ __forceinline__ void lay_out_costs(int B, long long (&warp_sum)[THREADS / 32], Cost&& cost, Locate&& locate) {
+    const int tid = (int)threadIdx.x;
+    const unsigned lane = lane_id(), warp = warp_id();
+    // the sum in front of this thread, *all the block's
+    auto scan = [&](long long x, long long* all) {
+        long long upto = x;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= (unsigned)o) upto += y;
+        }
+        if (lane == 31) warp_sum[warp] = upto;
+        __syncthreads();
+        long long before = 0, total = 0;
+#pragma unroll
+        for (int w = 0; w < THREADS / 32; ++w) {
+            if (w < (int)warp) before += warp_sum[w];
+            total += warp_sum[w];
+        }
+        __syncthreads();
+        *all = total;
+        return before + upto - x;
+    };
+    long long W = 0, mine = 0, before = 0;
+    for (int b0 = 0; b0 < B; b0 += THREADS) {
+        long long all;
+        mine = b0 + tid < B ? cost(b0 + tid) : 0;
+        before = scan(mine, &all);
+        W += all;
+    }
+    if (B <= THREADS) {
+        if (tid < B) locate(tid, before, mine, W);
+    } else {   // a second walk, now that W is known
+        long long base = 0;
+        for (int b0 = 0; b0 < B; b0 += THREADS) {
+            long long all;
+            const long long x = b0 + tid < B ? cost(b0 + tid) : 0;
+            const long long at = base + scan(x, &all);
+            if (b0 + tid < B) locate(b0 + tid, at, x, W);
+            base += all;
+        }
+    }
+}
+
 }  // namespace mea

@@ -193,52 +193,24 @@ struct Walk {
 
 // Every thread of the CTA: finds its share [W c / C, W (c + 1) / C) of the cost W of all items.
 __device__ __forceinline__ void find_share(const PagedTcArgs& a, Barriers* bars) {
-    const int tid = (int)threadIdx.x;
-    const unsigned lane = lane_id(), warp = warp_id();
+    if (threadIdx.x == 0) bars->share.cost = 0;
+    __syncthreads();
     Seq sq;
-    auto of_seq = [&](int b) {
+    auto cost = [&](int b) {
         sq = load_seq(a.s, b);
         const int items = items_of(sq, a.tt);
         long long sum = 0;
         for (int i = 0; i < items; ++i) sum += tiles_of(sq, a.tt, i) + kEndCost;
         return sum * a.Hkv;
     };
-    // inclusive scan over the block's threads; returns the sum in front of this thread, *all the block's
-    auto scan = [&](long long x, long long* all) {
-        long long upto = x;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= (unsigned)o) upto += y;
-        }
-        if (lane == 31) bars->warp_sum[warp] = upto;
-        __syncthreads();
-        long long before = 0, total = 0;
-#pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < (int)warp) before += bars->warp_sum[w];
-            total += bars->warp_sum[w];
-        }
-        __syncthreads();
-        *all = total;
-        return before + upto - x;
-    };
-    long long W = 0, mine = 0, block_before = 0;
-    for (int b0 = 0; b0 < a.s.B; b0 += kThreads) {
-        const int b = b0 + tid;
-        long long all;
-        mine = b < a.s.B ? of_seq(b) : 0;
-        block_before = scan(mine, &all);
-        W += all;
-    }
-    const long long w0 = W * blockIdx.x / gridDim.x, w1 = W * (blockIdx.x + 1) / gridDim.x;
-    if (tid == 0) bars->share.cost = w1 - w0;
-    auto locate = [&](int b, long long before, long long sum) {
+    auto locate = [&](int b, long long before, long long sum, long long W) {
+        const long long w0 = W * blockIdx.x / gridDim.x, w1 = W * (blockIdx.x + 1) / gridDim.x;
         if (w0 < before || w0 >= before + sum || w1 <= w0) return;
-        const int items = items_of(sq, a.tt);   // sq is b's since of_seq(b)
+        const int items = items_of(sq, a.tt);   // sq is b's since cost(b)
         const long long per_head = sum / a.Hkv;
         long long x = w0 - before;
         Barriers::Share& at = bars->share;
+        at.cost = w1 - w0;
         at.sq = sq;
         at.b = b;
         at.h = (int)(x / per_head);
@@ -252,19 +224,7 @@ __device__ __forceinline__ void find_share(const PagedTcArgs& a, Barriers* bars)
         at.i = i;
         at.t0 = (int)x;
     };
-    if (a.s.B <= kThreads) {
-        if (tid < a.s.B) locate(tid, block_before, mine);
-    } else {
-        long long base = 0;
-        for (int b0 = 0; b0 < a.s.B; b0 += kThreads) {
-            const int b = b0 + tid;
-            long long all;
-            const long long x = b < a.s.B ? of_seq(b) : 0;
-            const long long before = base + scan(x, &all);
-            if (b < a.s.B) locate(b, before, x);
-            base += all;
-        }
-    }
+    lay_out_costs<kThreads>(a.s.B, bars->warp_sum, cost, locate);
     __syncthreads();
 }
 

@@ -44,7 +44,6 @@ constexpr float kLog2e = 1.4426950408889634f;
 // D = 128 (six at D = 64), since decode is bound by the bytes in flight.
 constexpr int kFewRows = 16;
 constexpr int kMaxPairs = 6;
-constexpr int kMaxThreads = 608;
 
 template <int D, bool FEW>
 struct Cfg {
@@ -58,7 +57,7 @@ struct Cfg {
     static constexpr int kQStages = D == 128 && !FEW ? 2 : 4;
     static constexpr int kSmemData = 2 * kPairs * kTileBytes + kQStages * kQBytes;
     static constexpr int kLseBytes = kQStages * kTile * 4;
-    static constexpr int kSumBytes = 2 * kTile * 4;          // the second halves' sums
+    static constexpr int kSumBytes = 2 * kTile * 4;          // the second halves' sums; before, the warps' costs
     static constexpr int kSmemBytes = kSmemData + kLseBytes + kSumBytes + 1024 /*barriers*/ + 1024 /*alignment slack*/;
     static_assert(kSmemBytes <= 227 * 1024 && kPairs <= kMaxPairs, "shared memory");
 };
@@ -77,7 +76,6 @@ struct Barriers {
         int b, h, i, u0;
         long long units;
     } share;
-    long long warp_sum[kMaxThreads / 32];
 };
 
 __device__ __forceinline__ int q_tiles(const Seq& sq, int tt) { return (sq.n + tt - 1) / tt; }
@@ -144,54 +142,25 @@ struct Walk {
 };
 
 template <int THREADS>
-__device__ __forceinline__ void find_share(const PagedWeightsTcArgs& a, Barriers* bars) {
-    constexpr int kThreads = THREADS;
-    const int tid = (int)threadIdx.x;
-    const unsigned lane = lane_id(), warp = warp_id();
+__device__ __forceinline__ void find_share(const PagedWeightsTcArgs& a, Barriers* bars, long long (&warp_sum)[THREADS / 32]) {
+    if (threadIdx.x == 0) bars->share.units = 0;
+    __syncthreads();
     Seq sq;
-    auto of_seq = [&](int b) {
+    auto cost = [&](int b) {
         sq = load_seq(a.s, b);
         const int items = items_of(sq), full = full_items(sq);
         long long sum = (long long)full * q_tiles(sq, a.tt);
         for (int i = full; i < items; ++i) sum += units_of(sq, a.tt, i);
         return sum * a.Hkv;
     };
-    auto scan = [&](long long x, long long* all) {
-        long long upto = x;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= (unsigned)o) upto += y;
-        }
-        if (lane == 31) bars->warp_sum[warp] = upto;
-        __syncthreads();
-        long long before = 0, total = 0;
-#pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < (int)warp) before += bars->warp_sum[w];
-            total += bars->warp_sum[w];
-        }
-        __syncthreads();
-        *all = total;
-        return before + upto - x;
-    };
-    long long W = 0, mine = 0, block_before = 0;
-    for (int b0 = 0; b0 < a.s.B; b0 += kThreads) {
-        const int b = b0 + tid;
-        long long all;
-        mine = b < a.s.B ? of_seq(b) : 0;
-        block_before = scan(mine, &all);
-        W += all;
-    }
-    const long long c = blockIdx.x, C = gridDim.x;
-    const long long w0 = W * c / C, w1 = W * (c + 1) / C;
-    if (tid == 0) bars->share.units = w1 - w0;
-    auto locate = [&](int b, long long before, long long sum) {
+    auto locate = [&](int b, long long before, long long sum, long long W) {
+        const long long w0 = W * blockIdx.x / gridDim.x, w1 = W * (blockIdx.x + 1) / gridDim.x;
         if (w0 < before || w0 >= before + sum || w1 <= w0) return;
-        const int items = items_of(sq), full = full_items(sq), nq = q_tiles(sq, a.tt);   // sq is b's since of_seq(b)
+        const int items = items_of(sq), full = full_items(sq), nq = q_tiles(sq, a.tt);   // sq is b's since cost(b)
         const long long per_head = sum / a.Hkv;
         long long x = w0 - before;
         Barriers::Share& at = bars->share;
+        at.units = w1 - w0;
         at.sq = sq;
         at.b = b;
         at.h = (int)(x / per_head);
@@ -206,19 +175,7 @@ __device__ __forceinline__ void find_share(const PagedWeightsTcArgs& a, Barriers
         at.i = i;
         at.u0 = (int)x;
     };
-    if (a.s.B <= kThreads) {
-        if (tid < a.s.B) locate(tid, block_before, mine);
-    } else {
-        long long base = 0;
-        for (int b0 = 0; b0 < a.s.B; b0 += kThreads) {
-            const int b = b0 + tid;
-            long long all;
-            const long long x = b < a.s.B ? of_seq(b) : 0;
-            const long long before = base + scan(x, &all);
-            if (b < a.s.B) locate(b, before, x);
-            base += all;
-        }
-    }
+    lay_out_costs<THREADS>(a.s.B, warp_sum, cost, locate);
     __syncthreads();
 }
 
@@ -304,7 +261,7 @@ paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     volatile int* abort_flag = &bars->abort_flag;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    find_share<C::kThreads>(a, bars);
+    find_share<C::kThreads>(a, bars, *reinterpret_cast<long long(*)[C::kThreads / 32]>(sSum));
 
     Walk w;
     w.begin(a, bars);
