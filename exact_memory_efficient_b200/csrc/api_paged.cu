@@ -185,7 +185,6 @@ mea_status_t mea_rope(const void* x, void* y, const int* positions, const double
     if (B < 0 || H < 0 || N < 0) return invalid(where, "negative size");
     if ((st = check_rope(where, rot_dim, D, layout, mscale)) != MEA_OK) return st;
     if ((long long)B * H > 0x7fffffffLL || (long long)B * H * N >= (1LL << 40) / D) return invalid(where, "too many elements");
-    if (H > 65535) return api_fail(MEA_ERR_UNSUPPORTED, where, "at most 65535 heads");
     if ((long long)B * N > (1LL << 31) - 1) return api_fail(MEA_ERR_UNSUPPORTED, where, "B * N too large");
     if (B == 0 || H == 0 || N == 0) return MEA_OK;
     if (!x || !y || !positions || !freq) return invalid(where, "null pointer");

@@ -193,11 +193,14 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
 
 constexpr int kMoveThreads = 128;
 
-// Slot of kept key j in the destination pages.
+// Slot of kept key j in the destination pages.  Into other pages, one that is the
+// sequence's own page at the same place (the table's contents under another
+// pointer) would be overwritten while it is read: reported, not written.
 __device__ __forceinline__ size_t dst_slot(const EvictArgs& a, int b, int h, int j) {
     const int i = j >> a.s.page_shift;
     int p = i < a.dst_max_pages ? a.dst_table[(size_t)b * a.dst_max_pages + i] : -1;
-    if ((unsigned)p >= (unsigned)a.s.num_pages) {
+    if ((unsigned)p >= (unsigned)a.s.num_pages ||
+        (!a.in_place && i < a.s.max_pages && a.s.page_table[(size_t)b * a.s.max_pages + i] == p)) {
         flag_bad_page();
         return ~(size_t)0;   // not written
     }

@@ -241,7 +241,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a, in
 // heads 25.4.
 int heads_per_slice(long long threads_per_head, int H, int sm_count) {
     const long long per = threads_per_head * H / ((long long)sm_count * 768);
-    return per < 1 ? 1 : per > 16 ? 16 : (int)per;
+    const long long least = H / 32768 + 1;   // slices are a grid dimension of at most 65535
+    return (int)(per < least ? least : per > 16 ? (least > 16 ? least : 16) : per);
 }
 
 template <typename T, bool INTER>

@@ -124,6 +124,17 @@ class PagedCache:
         need = {s: max(0, -(-(self._len[s] + c) // self.page_size) - len(self._pages[s])) for s, c in zip(seqs, counts)}
         if sum(need.values()) > len(self._free):
             raise MemoryError(f"{sum(need.values())} pages needed, {len(self._free)} free")
+        before = [(s, len(self._pages[s]), self._len[s], self._pos[s]) for s in seqs]
+        try:
+            return self._step(q, k, v, seqs, counts, need, scale)
+        except Exception:   # a refused call leaves the page list as it was
+            for s, held, length, pos in before:
+                self._free.extend(reversed(self._pages[s][held:]))
+                del self._pages[s][held:]
+                self._len[s], self._pos[s] = length, pos
+            raise
+
+    def _step(self, q, k, v, seqs, counts, need, scale):
         cu, positions = [0], []
         for s, c in zip(seqs, counts):
             self._pages[s] += [self._free.pop() for _ in range(need[s])]

@@ -538,7 +538,9 @@ mea_status_t mea_attn_paged_weights(const void* q, const float* lse, const void*
  * lengths min(kv_len, n_keep).
  *
  * dst_table == page_table (the same pointer, dst_max_pages == max_pages): in
- * place.  Otherwise the destination pages must be none that the call reads.
+ * place.  Otherwise the destination pages must be none that the call reads; one
+ * that a sequence has at the same place of both tables (a copy of page_table) is
+ * not written and reported as MEA_ERR_PAGE.
  * No two sequences may share a destination page.  Keys keep the rotation of
  * their original positions.  0 <= n_recent <= n_keep, 1 <= n_keep;
  * B * H_kv <= 65535.  Errors: MEA_ERR_INVALID_ARG, MEA_ERR_UNSUPPORTED,

@@ -93,11 +93,11 @@ def test_rows_that_see_no_key(dtype, counts, lens):
 
 
 @pytest.mark.parametrize("garbage", [math.nan, math.inf, -math.inf])
-@pytest.mark.parametrize("dtype", [BF, F32])
-def test_garbage_behind_the_sequences(dtype, garbage):
+@pytest.mark.parametrize("dtype,page", [(BF, 16), (BF, 32), (BF, 128), (BF, 256), (F32, 32), (F32, 256)])
+def test_garbage_behind_the_sequences(dtype, page, garbage):
     """Free pages and the slots behind a sequence's last key may hold anything; rows outside every sequence too."""
-    for counts, lens in (([1, 1, 1], [17, 65, 300]), ([130, 5, 60], [131, 77, 60])):
-        bt = Batch(counts, lens, 4, 2, 128, 32, dtype, seed=2, garbage=garbage, front=1, behind=2)
+    for counts, lens in (([1, 1, 1, 1], [17, 65, 300, 200]), ([130, 5, 60, 260], [131, 77, 60, 330])):
+        bt = Batch(counts, lens, 4, 2, 128, page, dtype, seed=2, garbage=garbage, front=1, behind=2)
         bt.q[0] = garbage
         bt.q[-2:] = garbage
         check(bt, run(bt))

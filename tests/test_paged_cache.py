@@ -85,6 +85,24 @@ def test_refusals_change_nothing():
         assert (c.length(a), c.length(b), c.free_pages) == state
 
 
+def test_a_failing_step_leaves_the_page_list():
+    class Fails(OracleOps):
+        def attend(self, *args):
+            raise RuntimeError("launch")
+
+    c, g = cpu_cache(ops=Fails()), torch.Generator().manual_seed(7)
+    a, b = c.add(), c.add()
+    for _ in range(3):
+        with pytest.raises(RuntimeError):
+            c.step(*tokens(g, 50), [a, b], [33, 17])
+        assert (c.length(a), c.length(b), c.free_pages, c.pages(a)) == (0, 0, 12, [])
+    c.ops = OracleOps()
+    c.step(*tokens(g, 50), [a, b], [33, 17])
+    assert len(set(c.pages(a) + c.pages(b))) == 5 and c.free_pages == 7
+    c.step(*tokens(g, 0), [b], [0])      # nothing new: nothing changes
+    assert c.free_pages == 7
+
+
 def test_positions_run_on_after_an_eviction():
     """The rotation of the token after an eviction is that of its place in the sequence, not of its slot."""
     c, g = cpu_cache(), torch.Generator().manual_seed(3)

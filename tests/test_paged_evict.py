@@ -129,6 +129,11 @@ def test_evict_bad_tables_are_reported():
         y = {**dict(tab=tab, kv=kv, dst=dst), **x}
         m.paged_evict(kc, vc, w, y["tab"], y["kv"], y["dst"], 100, 10)
         assert m.mea_last_device_error() == m.MEA_ERR_PAGE
+    # a copy of the page table is not "in place": nothing is written over what is read
+    before = [t.clone() for t in (kc, vc, w)]
+    m.paged_evict(kc, vc, w, tab, kv, tab.clone(), 100, 10)
+    assert m.mea_last_device_error() == m.MEA_ERR_PAGE
+    assert all(torch.equal(x, y) for x, y in zip(before, (kc, vc, w)))
     m.paged_evict(kc, vc, w, tab, kv, dst, 100, 10)
     assert m.mea_last_device_error() == m.MEA_OK
 
@@ -139,3 +144,25 @@ def test_evict_many_sequences():
     bt = Batch([0] * 700, lens, 2, 2, 64, 16, BF, seed=10, spare=3000)
     check(bt, 40, 8)
     check(bt, 40, 8, in_place=True)
+
+
+def test_evict_more_candidates_than_shared_memory_holds():
+    """One CTA per head (75 of them) and more candidates than it can keep: the passes read the weights again."""
+    heads, L, page, keep = 75, 50001, 256, 30000
+    n = -(-L // page)
+    k = torch.zeros(n, heads, page, 64, dtype=BF, device="cuda")
+    w = torch.rand(n, heads, page, generator=torch.Generator().manual_seed(4))
+    w[:, 3] = (w[:, 3] * 4).floor()          # many ties
+    k[..., 0] = w.cuda().to(BF)              # a key that tells which one it was
+    order = torch.randperm(n, generator=torch.Generator().manual_seed(5)).int()
+    table = order.cuda()[None]
+    kept, length = m.paged_evict(k, k.clone(), w.clone().cuda(), table, torch.tensor([L], dtype=torch.int32).cuda(), table,
+                                 keep, 100)
+    assert length.item() == keep and m.mea_last_device_error() == m.MEA_OK
+    flat = w[order.long()].permute(1, 0, 2).reshape(heads, -1)[:, :L - 100]
+    best = torch.sort(flat, dim=1, descending=True, stable=True)[1][:, :keep - 100].sort(1)[0]
+    want = torch.cat([best, torch.arange(L - 100, L).expand(heads, -1)], 1)
+    assert torch.equal(kept[0].cpu().long(), want)
+    moved = k[order.cuda().long()].permute(1, 0, 2, 3).reshape(heads, -1, 64)[:, :keep, 0].cpu()
+    full = w[order.long()].permute(1, 0, 2).reshape(heads, -1).to(BF)
+    assert torch.equal(moved, full.gather(1, want))

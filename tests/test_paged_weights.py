@@ -62,9 +62,9 @@ def test_rows_that_see_nothing_add_nothing(dtype):
 
 
 @pytest.mark.parametrize("garbage", [math.nan, math.inf])
-@pytest.mark.parametrize("dtype", [BF, F32])
-def test_garbage_behind_the_sequences(dtype, garbage):
-    bt = Batch([1, 70, 3], [65, 130, 40], 4, 2, 128, 32, dtype, seed=4, garbage=garbage, front=1, behind=2)
+@pytest.mark.parametrize("dtype,page", [(BF, 16), (BF, 32), (BF, 128), (BF, 256), (F32, 32), (F32, 256)])
+def test_garbage_behind_the_sequences(dtype, page, garbage):
+    bt = Batch([1, 70, 3], [65, 130, 40], 4, 2, 128, page, dtype, seed=4, garbage=garbage, front=1, behind=2)
     bt.q[0] = garbage
     bt.q[-2:] = garbage
     lse = exact_lse(bt)
