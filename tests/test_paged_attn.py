@@ -296,7 +296,9 @@ def test_offsets_beyond_32_bits(dtype, D):
                                bt.scale)
     assert np.abs(f64(w[shift:]) - want).max() < 1e-3
     before = [x[shift:].cpu().float().numpy() for x in (*big, w)]
-    kept, n = m.paged_evict(*big, w, table.cuda(), kv, table.cuda(), 64, 16)
+    pages = table.cuda()          # in place: the same tensor twice, a copy of it is refused
+    kept, n = m.paged_evict(*big, w, pages, kv, pages, 64, 16)
+    assert m.mea_last_device_error() == 0
     ref = paged.evict(*before, bt.table.numpy(), bt.kv_len.numpy(), bt.table.numpy(), 64, 16)
     assert np.array_equal(kept.cpu().numpy(), ref[3]) and n.tolist() == [64, 64]
     for x, r in zip((*big, w), ref):
