@@ -5,7 +5,8 @@ The functions below carry the C names and only marshal arguments: tensor data
 pointers, sizes and the current CUDA stream.  Every step of the computation
 runs in the library's CUDA kernels; there is no CPU or PyTorch fallback, and
 loading fails loudly if the library has not been built.  PyTorch is used only
-to own device memory and streams.
+to own device memory and streams.  The rotary and paged-cache functions go
+through the compiled binding (csrc/binding.cpp), the others through ctypes.
 
     o, lse = attention_forward(q, k, v)                 # allocates o, lse
     dq, dk, dv = attention_backward(q, k, v, o, lse, do)  # allocates grads + workspace
@@ -30,7 +31,7 @@ import os
 import torch
 
 __all__ = [
-    "MeaError", "load_library", "library_path",
+    "MeaError", "load_library", "load_binding", "library_path",
     "MEA_OK", "MEA_ERR_INVALID_ARG", "MEA_ERR_UNSUPPORTED", "MEA_ERR_MISALIGNED", "MEA_ERR_WORKSPACE",
     "MEA_ERR_CUDA", "MEA_ERR_TIMEOUT", "MEA_ERR_PAGE", "MEA_DTYPE_F32", "MEA_DTYPE_BF16",
     "MEA_BWD_ALL", "MEA_BWD_PREPROCESS", "MEA_BWD_MAIN", "MEA_BWD_FINALIZE", "MEA_NOALLOC_SCRATCH_BYTES",
@@ -475,122 +476,42 @@ def mea_rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: int = MEA
     return torch.tensor(list(out), dtype=torch.float64)
 
 
-def _bad(where: str, what: str):
-    raise MeaError(MEA_ERR_INVALID_ARG, f"{where}: {what}")
+_BINDING = None
 
 
-def _same_device(where: str, first, named) -> int:
-    """Index of ``first``'s CUDA device; every other tensor on it, dense and of the given dtype."""
-    dev = first.get_device()
-    if dev < 0:
-        _bad(where, "CUDA tensors")
-    for name, t, dtype in named:
-        if t is not None and (t.get_device() != dev or t.dtype != dtype or not t.is_contiguous()):
-            if t.get_device() != dev:
-                _bad(where, f"{name} is not on the device of the first tensor")
-            _bad(where, f"{name} must be {dtype}" if t.dtype != dtype else f"{name} must be contiguous")
-    return dev
+def load_binding():
+    """The compiled binding of the entry points below (raises if it is missing)."""
+    global _BINDING
+    if _BINDING is not None:
+        return _BINDING
+    load_library()
+    try:
+        from . import _binding
+    except ImportError as e:
+        raise RuntimeError(
+            "_binding.so is missing or does not fit this interpreter: build it with "
+            "`python -m exact_memory_efficient_b200.build` (there is no fallback implementation)") from e
+    _binding.set_error(MeaError)
+    _BINDING = _binding
+    return _binding
 
 
-def _packed(where: str, name: str, t, dtype, T=None, heads=None, D=None) -> int:
-    """Token stride of packed [T, heads, D] rows: heads and dims dense, any token stride."""
-    if t.dim() != 3 or t.dtype != dtype:
-        _bad(where, f"{name} shape/dtype mismatch")
-    n, h, d = t.shape
-    if (T is not None and n != T) or (heads is not None and h != heads) or (D is not None and d != D):
-        _bad(where, f"{name} shape/dtype mismatch")
-    token, head, dim = t.stride()
-    if (d > 1 and dim != 1) or (h > 1 and head != d):
-        _bad(where, f"{name}: heads and head dims must be dense")
-    return token if n > 1 else h * d
-
-
-def _pages(where: str, k_cache, v_cache=None, weights=None, like=None):
-    """Sizes of a cache [pages, H_kv, page_size, D]; v_cache alike, weights [pages, H_kv, page_size] fp32."""
-    if k_cache.dim() != 4:
-        _bad(where, "k_cache must be [pages, H_kv, page_size, D]")
-    if like is not None and like.dtype != k_cache.dtype:
-        _bad(where, "k_cache dtype mismatch")
-    if v_cache is not None and v_cache.shape != k_cache.shape:
-        _bad(where, "v_cache must be shaped like k_cache")
-    if weights is not None and weights.shape != k_cache.shape[:3]:
-        _bad(where, "weights must be [pages, H_kv, page_size]")
-    return k_cache.shape
-
-
-def _batch(where: str, kv_len, page_table, cu_q=None):
-    if kv_len.dim() != 1 or page_table.dim() != 2 or page_table.shape[0] != kv_len.shape[0]:
-        _bad(where, "kv_len must be [B] and page_table [B, max_pages]")
-    if cu_q is not None and tuple(cu_q.shape) != (kv_len.shape[0] + 1,):
-        _bad(where, "cu_q must be [B + 1]")
-    return page_table.shape
-
-
-def _launch(where: str, fn, device: int, stream, *args) -> None:
-    """fn(*args, stream) with the device current (its current stream where none is given)."""
-    if device != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return _launch(where, fn, device, stream, *args)
-    st = fn(*args, _raw_stream(device) if stream is None else _stream_handle(stream))
-    if st != MEA_OK:
-        raise MeaError(st, where)
-
-
-def _raw_stream(device: int) -> int:
-    """Handle of the device's current stream (without building a torch.cuda.Stream for it: 0.1 against 3 us)."""
-    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return int(get(device)) if get is not None else int(torch.cuda.current_stream(device).cuda_stream)
-
-
-def _dense(shape):
-    """Strides of a contiguous tensor."""
-    n = len(shape)
-    if n == 1:
-        return (1,)
-    if n == 2:
-        return (shape[1], 1)
-    if n == 3:
-        return (shape[1] * shape[2], shape[2], 1)
-    return (shape[1] * shape[2] * shape[3], shape[2] * shape[3], shape[3], 1)
-
-
-def _empty(stream, like, *shapes):
-    """Tensors of the (shape, dtype) pairs on ``like``'s device, allocated on ``stream`` where one is
-    given, so that the allocator does not hand their memory on while the call may still run."""
-    if stream is None:
-        dev, make = like.device, torch.empty_strided     # the cheapest of torch's allocations
-        return [make(shape, _dense(shape), dtype=dtype, device=dev) if shape is not None else None
-                for shape, dtype in shapes]
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(_stream_handle(stream), device=like.device)
-    with torch.cuda.stream(stream):
-        return _empty(None, like, *shapes)
+def _layout(interleaved: bool) -> int:
+    return MEA_ROPE_INTERLEAVED if interleaved else MEA_ROPE_HALF
 
 
 def mea_rope(x, y, positions, freq, layout: int = MEA_ROPE_HALF, mscale: float = 1.0, inverse: bool = False,
              stream=None) -> None:
     """C ``mea_rope``: y = mscale * R(positions) x on x [B,H,N,D] (y may be x); positions int32 [N] or
     [B,N]; freq fp64 [rot_dim / 2] on the device; ``inverse`` is the gradient's direction."""
-    B, H, N, D = _shape4(x, "x")
-    if y.shape != x.shape or y.dtype != x.dtype:
-        _bad("mea_rope", "y shape/dtype mismatch")
-    if freq.dim() != 1:
-        _bad("mea_rope", "freq must be [rot_dim / 2]")
-    if tuple(positions.shape) not in ((N,), (B, N)):
-        _bad("mea_rope", "positions must be [N] or [B, N]")
-    dev = _same_device("mea_rope", x, (("x", x, x.dtype), ("y", y, x.dtype), ("positions", positions, torch.int32),
-                                       ("freq", freq, torch.float64)))
-    _launch("mea_rope", load_library().mea_rope, dev, stream, x.data_ptr(), y.data_ptr(), positions.data_ptr(),
-            freq.data_ptr(), B, H,
-            N, D, 2 * freq.shape[0], int(positions.dim() == 2), int(layout), float(mscale), int(bool(inverse)),
-            _dtype_code(x))
+    if y is None:
+        raise MeaError(MEA_ERR_INVALID_ARG, "mea_rope: y")
+    load_binding().rope(x, y, positions, freq, layout, mscale, inverse, stream)
 
 
 def rope(x, positions, freq, interleaved: bool = False, mscale: float = 1.0, inverse: bool = False, stream=None):
     """Allocate y with torch and run ``mea_rope``; the gradient of x is ``rope(dy, ..., inverse=True)``."""
-    y, = _empty(stream, x, (x.shape, x.dtype))
-    mea_rope(x, y, positions, freq, MEA_ROPE_INTERLEAVED if interleaved else MEA_ROPE_HALF, mscale, inverse, stream)
-    return y
+    return load_binding().rope(x, None, positions, freq, _layout(interleaved), mscale, inverse, stream)
 
 
 def mea_paged_append(q, q_out, k, v, k_cache, v_cache, weights, cu_q, kv_len, page_table, positions=None, freq=None,
@@ -598,45 +519,16 @@ def mea_paged_append(q, q_out, k, v, k_cache, v_cache, weights, cu_q, kv_len, pa
     """C ``mea_paged_append``: k turned and v go to the sequences' last slots, q turned to q_out.  q and
     q_out may be None (keys only), weights None (none kept), positions None (the slots), freq None (no
     rotation)."""
-    w = "mea_paged_append"
-    pages, Hkv, page, D = _pages(w, k_cache, v_cache, weights)
-    B, max_pages = _batch(w, kv_len, page_table, cu_q)
-    dt = k_cache.dtype
-    ks = _packed(w, "k", k, dt, None, Hkv, D)
-    T = k.shape[0]
-    vs = _packed(w, "v", v, dt, T, Hkv, D)
-    if (q is None) != (q_out is None):
-        _bad(w, "q and q_out go together")
-    H, qs = 0, 0
-    if q is not None:
-        qs, H = _packed(w, "q", q, dt, T, None, D), q.shape[1]
-        if q_out.shape != q.shape:
-            _bad(w, "q_out must be shaped like q")
-    if positions is not None and tuple(positions.shape) != (T,):
-        _bad(w, "positions must be [T]")
-    if freq is not None and freq.dim() != 1:
-        _bad(w, "freq must be [rot_dim / 2]")
-    dev = _same_device(w, k, (("k_cache", k_cache, dt), ("v_cache", v_cache, dt), ("weights", weights, torch.float32),
-                        ("cu_q", cu_q, torch.int32), ("kv_len", kv_len, torch.int32),
-                        ("page_table", page_table, torch.int32), ("positions", positions, torch.int32),
-                        ("freq", freq, torch.float64), ("q_out", q_out, dt)))
-    if v.get_device() != dev or (q is not None and q.get_device() != dev):
-        _bad(w, "q, k and v must be on one device")
-    _launch(w, load_library().mea_paged_append, dev, stream, _ptr(q), _ptr(q_out), k.data_ptr(), v.data_ptr(),
-            k_cache.data_ptr(), v_cache.data_ptr(), _ptr(weights), cu_q.data_ptr(), kv_len.data_ptr(),
-            page_table.data_ptr(), _ptr(positions),
-            _ptr(freq), T, B, H, Hkv, D, qs, ks, vs, pages, page, max_pages, 0 if freq is None else 2 * freq.shape[0],
-            int(layout), float(mscale), _dtype_code(k_cache))
+    load_binding().append(q, q_out, False, k, v, k_cache, v_cache, weights, cu_q, kv_len, page_table, positions, freq,
+                          layout, mscale, stream)
 
 
 def paged_append(q, k, v, k_cache, v_cache, weights, cu_q, kv_len, page_table, positions=None, freq=None,
                  interleaved: bool = False, mscale: float = 1.0, stream=None):
     """Allocate the turned q with torch and run ``mea_paged_append``; returns it (None without q).  Rows
     outside every sequence are not written."""
-    q_out = None if q is None else _empty(stream, q, (q.shape, q.dtype))[0]
-    mea_paged_append(q, q_out, k, v, k_cache, v_cache, weights, cu_q, kv_len, page_table, positions, freq,
-                     MEA_ROPE_INTERLEAVED if interleaved else MEA_ROPE_HALF, mscale, stream)
-    return q_out
+    return load_binding().append(q, None, True, k, v, k_cache, v_cache, weights, cu_q, kv_len, page_table, positions,
+                                 freq, _layout(interleaved), mscale, stream)
 
 
 def _paged_workspace(where: str, fn, sizes, dtype) -> int:
@@ -660,62 +552,20 @@ def mea_attn_paged_weights_workspace_size(T: int, B: int, H: int, H_kv: int, D: 
                             (T, B, H, H_kv, D, max_q, max_kv), dtype)
 
 
-def _workspace_bytes(where: str, workspace, device: int) -> int:
-    if workspace is None:
-        return 0
-    if workspace.get_device() != device or not workspace.is_contiguous():
-        _bad(where, "workspace must be a contiguous tensor on the device")
-    return workspace.numel() * workspace.element_size()
-
-
 def mea_attn_paged(q, k_cache, v_cache, o, lse, cu_q, kv_len, page_table, max_q: int, max_kv: int, scale: float,
                    workspace, stream=None) -> None:
     """C ``mea_attn_paged``: q [T,H,D] (any token stride) over the pages; writes o [T,H,D] and lse [T,H]
     (fp32).  ``workspace`` a CUDA tensor of at least ``mea_attn_paged_workspace_size`` bytes (None when 0)."""
-    w = "mea_attn_paged"
-    pages, Hkv, page, D = _pages(w, k_cache, v_cache, like=q)
-    B, max_pages = _batch(w, kv_len, page_table, cu_q)
-    dt = k_cache.dtype
-    qs = _packed(w, "q", q, dt, None, None, D)
-    T, H = q.shape[:2]
-    if o.shape != q.shape or tuple(lse.shape) != (T, H):
-        _bad(w, "o must be shaped like q, lse [T, H]")
-    dev = _same_device(w, q, (("k_cache", k_cache, dt), ("v_cache", v_cache, dt), ("o", o, dt), ("lse", lse, torch.float32),
-                        ("cu_q", cu_q, torch.int32), ("kv_len", kv_len, torch.int32),
-                        ("page_table", page_table, torch.int32)))
-    ws_bytes = _workspace_bytes(w, workspace, dev)
-    _launch(w, load_library().mea_attn_paged, dev, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-            o.data_ptr(),
-            lse.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), T, B, H, Hkv, D, qs, pages,
-            page, max_pages,
-            int(max_q), int(max_kv), float(scale), _dtype_code(q), _ptr(workspace), ws_bytes)
-
-
-def _paged_call(where: str, size, q, k_cache, kv_len, max_q: int, max_kv: int, scale):
-    """T, H, D, workspace bytes and scale of a call that allocates for itself."""
-    if q.dim() != 3 or k_cache.dim() != 4 or kv_len.dim() != 1:
-        _bad(where, "q must be [T, H, D], k_cache [pages, H_kv, page_size, D] and kv_len [B]")
-    if not q.is_cuda:
-        _bad(where, "CUDA tensors")
-    T, H, D = q.shape
-    sizes = (T, kv_len.shape[0], H, k_cache.shape[1], D, max_q, max_kv, q.dtype)
-    if q.get_device() == torch.cuda.current_device():
-        n = size(*sizes)
-    else:
-        with torch.cuda.device(q.device):
-            n = size(*sizes)
-    return T, H, D, n, 1.0 / math.sqrt(D) if scale is None else scale
+    load_binding().attend(q, k_cache, v_cache, o, lse, False, cu_q, kv_len, page_table, max_q, max_kv, scale, workspace,
+                          stream)
 
 
 def attention_paged(q, k_cache, v_cache, cu_q, kv_len, page_table, max_q: int, max_kv: int,
                     scale: float | None = None, stream=None):
     """Allocate (o, lse) and the workspace with torch and run ``mea_attn_paged``.  Rows outside every
     sequence are not written."""
-    T, H, D, n, scale = _paged_call("attention_paged", mea_attn_paged_workspace_size, q, k_cache, kv_len, max_q, max_kv,
-                                    scale)
-    o, lse, ws = _empty(stream, q, ((T, H, D), q.dtype), ((T, H), torch.float32), ((n,) if n else None, torch.uint8))
-    mea_attn_paged(q, k_cache, v_cache, o, lse, cu_q, kv_len, page_table, max_q, max_kv, scale, ws, stream)
-    return o, lse
+    return load_binding().attend(q, k_cache, v_cache, None, None, True, cu_q, kv_len, page_table, max_q, max_kv, scale,
+                                 None, stream)
 
 
 def mea_attn_paged_weights(q, lse, k_cache, weights, cu_q, kv_len, page_table, max_q: int, max_kv: int, scale: float,
@@ -723,67 +573,28 @@ def mea_attn_paged_weights(q, lse, k_cache, weights, cu_q, kv_len, page_table, m
     """C ``mea_attn_paged_weights``: adds to weights [pages,H_kv,page_size] what every cached key's
     probabilities sum to over the rows of the call (lse [T,H] from ``mea_attn_paged``).  ``workspace`` of
     ``mea_attn_paged_weights_workspace_size`` bytes (None when 0)."""
-    w = "mea_attn_paged_weights"
-    pages, Hkv, page, D = _pages(w, k_cache, None, weights, q)
-    B, max_pages = _batch(w, kv_len, page_table, cu_q)
-    qs = _packed(w, "q", q, k_cache.dtype, None, None, D)
-    T, H = q.shape[:2]
-    if tuple(lse.shape) != (T, H):
-        _bad(w, "lse must be [T, H]")
-    dev = _same_device(w, q, (("k_cache", k_cache, k_cache.dtype), ("weights", weights, torch.float32),
-                        ("lse", lse, torch.float32), ("cu_q", cu_q, torch.int32), ("kv_len", kv_len, torch.int32),
-                        ("page_table", page_table, torch.int32)))
-    _launch(w, load_library().mea_attn_paged_weights, dev, stream, q.data_ptr(), lse.data_ptr(), k_cache.data_ptr(),
-            weights.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), T, B, H, Hkv, D, qs,
-            pages, page, max_pages,
-            int(max_q), int(max_kv), float(scale), _dtype_code(q), _ptr(workspace),
-            _workspace_bytes(w, workspace, dev))
+    load_binding().weigh(q, lse, k_cache, weights, False, cu_q, kv_len, page_table, max_q, max_kv, scale, workspace,
+                         stream)
 
 
 def attention_paged_weights(q, lse, k_cache, weights, cu_q, kv_len, page_table, max_q: int, max_kv: int,
                             scale: float | None = None, stream=None) -> None:
     """Allocate the workspace with torch and run ``mea_attn_paged_weights``."""
-    _, _, _, n, scale = _paged_call("attention_paged_weights", mea_attn_paged_weights_workspace_size, q, k_cache, kv_len,
-                                    max_q, max_kv, scale)
-    ws, = _empty(stream, q, ((n,) if n else None, torch.uint8))
-    mea_attn_paged_weights(q, lse, k_cache, weights, cu_q, kv_len, page_table, max_q, max_kv, scale, ws, stream)
+    load_binding().weigh(q, lse, k_cache, weights, True, cu_q, kv_len, page_table, max_q, max_kv, scale, None, stream)
 
 
 def mea_paged_evict(k_cache, v_cache, weights, page_table, kv_len, dst_table, kv_len_out, keep_idx, n_recent: int,
                     stream=None) -> None:
     """C ``mea_paged_evict``: cuts sequences to keep_idx.shape[2] keys, moved to the pages of dst_table
     (``page_table`` itself: in place); writes keep_idx [B,H_kv,n_keep] and kv_len_out [B] (int32, or None)."""
-    w = "mea_paged_evict"
-    pages, Hkv, page, D = _pages(w, k_cache, v_cache, weights)
-    B, max_pages = _batch(w, kv_len, page_table)
-    if dst_table.dim() != 2 or dst_table.shape[0] != B:
-        _bad(w, "dst_table must be [B, dst_max_pages]")
-    if keep_idx.dim() != 3 or tuple(keep_idx.shape[:2]) != (B, Hkv):
-        _bad(w, "keep_idx must be [B, H_kv, n_keep]")
-    if kv_len_out is not None and kv_len_out.shape != kv_len.shape:
-        _bad(w, "kv_len_out must be [B]")
-    i32 = torch.int32
-    dev = _same_device(w, k_cache, (("k_cache", k_cache, k_cache.dtype), ("v_cache", v_cache, k_cache.dtype),
-                              ("weights", weights, torch.float32), ("page_table", page_table, i32),
-                              ("kv_len", kv_len, i32), ("dst_table", dst_table, i32), ("keep_idx", keep_idx, i32),
-                              ("kv_len_out", kv_len_out, i32)))
-    _launch(w, load_library().mea_paged_evict, dev, stream, k_cache.data_ptr(), v_cache.data_ptr(), weights.data_ptr(),
-            page_table.data_ptr(), kv_len.data_ptr(), dst_table.data_ptr(), _ptr(kv_len_out), keep_idx.data_ptr(), B,
-            Hkv, D, pages, page,
-            max_pages, dst_table.shape[1], keep_idx.shape[2], int(n_recent), _dtype_code(k_cache))
+    load_binding().evict(k_cache, v_cache, weights, page_table, kv_len, dst_table, kv_len_out, keep_idx, None, n_recent,
+                         stream)
 
 
 def paged_evict(k_cache, v_cache, weights, page_table, kv_len, dst_table, n_keep: int, n_recent: int, stream=None):
     """Allocate (keep_idx, kv_len_out) with torch and run ``mea_paged_evict``."""
-    _pages("paged_evict", k_cache)
-    if n_keep < 1:
-        _bad("paged_evict", "n_keep below 1")
-    if not k_cache.is_cuda:
-        _bad("paged_evict", "CUDA tensors")
-    B = kv_len.shape[0]
-    idx, out = _empty(stream, k_cache, ((B, k_cache.shape[1], n_keep), torch.int32), ((B,), torch.int32))
-    mea_paged_evict(k_cache, v_cache, weights, page_table, kv_len, dst_table, out, idx, n_recent, stream)
-    return idx, out
+    return load_binding().evict(k_cache, v_cache, weights, page_table, kv_len, dst_table, None, None, n_keep, n_recent,
+                                stream)
 
 
 def mea_selftest_bounded_wait(gave_up, stream=None) -> None:

@@ -3,9 +3,13 @@
     python -m exact_memory_efficient_b200.build [--force] [--verbose]
 
 The library is a plain C-ABI shared object (see include/mea_attn.h); nothing
-here depends on torch.  Objects are compiled in parallel and linked with nvcc
+in it depends on torch.  Objects are compiled in parallel and linked with nvcc
 (relocatable device code, so the per-device error word is shared by all
 kernels).  The CUDA runtime is linked statically.
+
+_binding.so beside it is the CPython binding of the rotary and paged-cache
+entry points for torch tensors (csrc/binding.cpp), compiled against the torch
+and Python of the running interpreter and linked to the library.
 """
 
 from __future__ import annotations
@@ -28,6 +32,9 @@ LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 SOURCES = ["api.cu", "fwd_f32.cu", "bwd_f32.cu", "fwd_bf16.cu", "fwd_persist.cu", "bwd_bf16.cu", "combine.cu", "decode.cu",
            "api_paged.cu", "rope.cu", "paged_attn.cu", "paged_tc.cu", "paged_weights.cu", "paged_weights_tc.cu", "paged_evict.cu"]
 HEADERS = ["ptx.cuh", "kernels.h", "simt_f32.cuh", "rows.cuh", "paged.cuh", "api_internal.h"]
+
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING_PATH = os.path.join(PKG_DIR, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-rdc=true", "-Xcompiler", "-fPIC",
@@ -65,7 +72,46 @@ def _compile(nvcc: str, src: str, verbose: bool, extra: list[str]) -> str:
     return obj
 
 
+def needs_binding() -> bool:
+    src = max(os.path.getmtime(f) for f in (BINDING_SRC, os.path.join(INCLUDE, "mea_attn.h"), os.path.abspath(__file__)))
+    return not os.path.exists(BINDING_PATH) or os.path.getmtime(BINDING_PATH) < src
+
+
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    """Compile _binding.so (needs the library)."""
+    if not force and not needs_binding():
+        return BINDING_PATH
+    import sysconfig
+
+    import torch
+    torch_dir = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc_path()))
+    includes = [os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+                sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE]
+    tmp = BINDING_PATH + ".tmp"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[x for p in includes for x in ("-isystem" if p != INCLUDE else "-I", p)], BINDING_SRC, "-o", tmp,
+           "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+           "-L", PKG_DIR, f"-l:{LIB_NAME}", "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0 or verbose:
+        sys.stderr.write(r.stdout + r.stderr)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed on binding.cpp")
+    os.replace(tmp, BINDING_PATH)
+    return BINDING_PATH
+
+
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
+    _build_library(force, verbose, extra)
+    build_binding(force, verbose)
+    return LIB_PATH
+
+
+def _build_library(force: bool, verbose: bool, extra: list[str] | None) -> str:
     if not force and not needs_build():
         return LIB_PATH
     nvcc = nvcc_path()
