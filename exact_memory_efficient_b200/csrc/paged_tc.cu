@@ -625,8 +625,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     uint32_t pk[16];
 #pragma unroll
                     for (int c = 0; c < 32; c += 2) {
-                        const float p0 = ex2_approx(fmaf(__uint_as_float(sr[c0 + c]), c_log2, -m_ref));
-                        const float p1 = ex2_approx(fmaf(__uint_as_float(sr[c0 + c + 1]), c_log2, -m_ref));
+                        float p0 = -m_ref, p1 = -m_ref;
+                        fma2(p0, p1, __uint_as_float(sr[c0 + c]), __uint_as_float(sr[c0 + c + 1]), c_log2, c_log2);
+                        p0 = ex2_approx(p0);
+                        p1 = ex2_approx(p1);
                         rsa[(c / 2) & 7] += p0 + p1;
                         pk[c / 2] = pack_bf16x2(p0, p1);
                     }
@@ -779,109 +781,174 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     }
 }
 
-// Joins the parts of the item that share blockIdx.x of the main kernel began and
-// did not finish: the first in one of its own slots, the others in the first
-// slots of the shares behind it.  grid.y: slices of the item's rows.  W warps take
-// a row, each every W-th part, a lane D / 32 head dims; the warps' results are
-// joined through shared memory (W = 8 where an item has few rows: decode cuts a
-// long cache into many parts).
+// Joins the parts of the items that shares of the main kernel began and did not
+// finish.  A share has a part in its first slot, its second, both or none; taken
+// share by share they are in the order of the work, so an item's parts follow one
+// another, the first with t0 = 0.  Every CTA lists them (a share per thread) and
+// takes slices of kRows rows of the items: W warps take R rows, each every W-th
+// part, a lane D / 32 head dims; the warps' results are joined through shared memory
+// (W = 8, R = 1 where an item has few rows: decode cuts a long cache into many parts).
+// The slices' first rows come first: an item that is not full leaves the last idle.
+// Bound: launch, the look-up (2 us) and a round of loads; from 20 MB of parts on L2.
+// With a CTA per share and slice, most of them idle, and every part's loads behind a
+// look-up and the exponential of the part in front, 60 tokens over 1000 keys (8 parts
+// an item) took 28.9 us, now 17.4 (12.5 without this kernel); 8 prompts of 97 to 500
+// tokens 33.5, now 29.4.  More CTAs per SM spill or wait for one another's registers.
 constexpr int kMergeThreads = 256;
 constexpr int kMergeBatch = 4;
+constexpr int kMergeBlocks = 2, kMergeBlocksFew = 3;   // per SM
 
-template <int DPL, int W>
-__global__ void __launch_bounds__(kMergeThreads) paged_tc_merge_kernel(const PagedTcArgs a, int shares) {
+// Loads that the compiler leaves where they are (it sinks plain ones to their uses,
+// each behind the exponential of the part in front).
+__device__ __forceinline__ void load_now(const float* p, float2& x) {
+    asm volatile("ld.global.v2.f32 {%0, %1}, [%2];" : "=f"(x.x), "=f"(x.y) : "l"(p));
+}
+__device__ __forceinline__ void load_now(const float* p, float (&x)[2]) {
+    asm volatile("ld.global.v2.f32 {%0, %1}, [%2];" : "=f"(x[0]), "=f"(x[1]) : "l"(p));
+}
+__device__ __forceinline__ void load_now(const float* p, float (&x)[4]) {
+    asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]) : "l"(p));
+}
+
+template <int DPL, int W, int R>
+__global__ void __launch_bounds__(kMergeThreads, W > 1 ? kMergeBlocksFew : kMergeBlocks) paged_tc_merge_kernel(const PagedTcArgs a, int shares) {
     constexpr int D = 32 * DPL;
-    constexpr int kRows = kMergeThreads / 32 / W;     // rows at a time
-    __shared__ float s_acc[W > 1 ? W : 1][D];
-    __shared__ float2 s_ml[W > 1 ? W : 1];
+    constexpr int kWarps = kMergeThreads / 32;
+    constexpr int kRows = kWarps / W * R;
+    struct Split {
+        int at;               // its first part in s_slot
+        int n, q0, h, tok0;   // new tokens of the sequence, its first packed row; head; first token
+    };
+    __shared__ int s_parts[kWarps], s_items[kWarps];
+    __shared__ int s_slot[2 * kMergeThreads];
+    __shared__ Split s_item[kMergeThreads + 1];
+    __shared__ float s_acc[W > 1 ? kWarps : 1][D];
+    __shared__ float2 s_ml[W > 1 ? kWarps : 1];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int c0 = (int)blockIdx.x;
     const int warp = (int)warp_id(), lane = (int)lane_id();
-    const PagedPart p0 = a.parts[2 * c0], p1 = a.parts[2 * c0 + 1];
-    const int slot = 2 * c0 + (p0.n_kv != 0 && p0.t0 == 0 ? 0 : 1);
-    const PagedPart p = slot == 2 * c0 ? p0 : p1;
-    if (p.n_kv == 0 || p.t0 != 0 || p.t1 == p.n_kv) return;
-    // the share that holds the last part; with little work some between have none
-    int c1 = shares - 1;
-    for (int c = c0 + 1; c < shares; c += 32) {
-        bool end = false;
-        if (c + lane < shares) {
-            const PagedPart n = a.parts[2 * (c + lane)];
-            end = n.n_kv != 0 && n.t1 == n.n_kv;
-        }
-        const unsigned ends = __ballot_sync(0xffffffffu, end);
-        if (ends) {
-            c1 = c + __ffs((int)ends) - 1;
-            break;
-        }
+    PagedPart p0 = {}, p1 = {};
+    if ((int)threadIdx.x < shares) {
+        p0 = a.parts[2 * threadIdx.x];
+        p1 = a.parts[2 * threadIdx.x + 1];
     }
+    const bool has0 = p0.n_kv != 0, has1 = p1.n_kv != 0;
+    const bool first0 = has0 && p0.t0 == 0, first1 = has1 && p1.t0 == 0;   // at most one of them
+    const unsigned below = (1u << lane) - 1u;
+    const unsigned b0 = __ballot_sync(0xffffffffu, has0), b1 = __ballot_sync(0xffffffffu, has1);
+    const unsigned bf = __ballot_sync(0xffffffffu, first0 || first1);
+    if (lane == 0) {
+        s_parts[warp] = __popc(b0) + __popc(b1);
+        s_items[warp] = __popc(bf);
+    }
+    __syncthreads();
+    int at = __popc(b0 & below) + __popc(b1 & below), item = __popc(bf & below), parts = 0, items = 0;
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) {
+        at += k < warp ? s_parts[k] : 0;
+        item += k < warp ? s_items[k] : 0;
+        parts += s_parts[k];
+        items += s_items[k];
+    }
+    if (has0) s_slot[at] = 2 * (int)threadIdx.x;
+    if (has1) s_slot[at + has0] = 2 * (int)threadIdx.x + 1;
+    if (first0 || first1) {
+        const PagedPart& p = first0 ? p0 : p1;
+        s_item[item] = {at + (first0 ? 0 : (int)has0), p.n, p.q0, p.h, p.i * 2 * a.tt};
+    }
+    if (threadIdx.x == 0) s_item[items].at = parts;
+    __syncthreads();
     const int G = a.H / a.Hkv;
     const int rows = 2 * a.tt * G;
-    const int per = (rows + (int)gridDim.y - 1) / (int)gridDim.y;
-    const int wi = warp % W;
-    for (int r0 = (int)blockIdx.y * per; r0 < min(rows, ((int)blockIdx.y + 1) * per); r0 += kRows) {
-        const int r = r0 + warp / W;
-        const int tok = p.i * 2 * a.tt + r / G;
-        if (r >= min(rows, ((int)blockIdx.y + 1) * per) || tok >= p.n) break;   // W > 1: the same for all warps
-        float M = -INFINITY, L = 0.f, A[DPL];
+    const int slices = (rows + kRows - 1) / kRows;
+    for (int unit = (int)blockIdx.x; unit < items * slices; unit += (int)gridDim.x) {
+        const Split p = s_item[unit % items];
+        const int* slot = s_slot + p.at;
+        const int count = s_item[unit % items + 1].at - p.at;
+        const int row0 = unit / items * kRows;
+        if (p.tok0 + row0 / G >= p.n) continue;
+        const int wi = warp % W;
+        float M[R], L[R], A[R][DPL];
+        int r[R];
 #pragma unroll
-        for (int i = 0; i < DPL; ++i) A[i] = 0.f;
-        for (int c = c0 + wi; c <= c1; c += W * kMergeBatch) {
-            float mc[kMergeBatch], lc[kMergeBatch], x[kMergeBatch][DPL];
+        for (int k = 0; k < R; ++k) {
+            r[k] = row0 + warp / W * R + k;
+            M[k] = -INFINITY;
+            L[k] = 0.f;
+#pragma unroll
+            for (int i = 0; i < DPL; ++i) A[k][i] = 0.f;
+        }
+        for (int n0 = wi; n0 < count; n0 += W * kMergeBatch) {
+            float2 ml[kMergeBatch][R];
+            float x[kMergeBatch][R][DPL];
 #pragma unroll
             for (int u = 0; u < kMergeBatch; ++u) {
-                const int cu = c + u * W;
-                mc[u] = -INFINITY;
-                if (cu <= c1 && (cu == c0 || a.parts[2 * cu].n_kv != 0)) {
-                    const size_t row = (size_t)(cu == c0 ? slot : 2 * cu) * rows + r;
-                    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + 2 * row);
-                    mc[u] = ml.x;
-                    lc[u] = ml.y;
-                    load_row(a.part_acc + row * D + lane * DPL, x[u]);
+                const size_t base = (size_t)slot[min(n0 + u * W, count - 1)] * rows;
+#pragma unroll
+                for (int k = 0; k < R; ++k) {
+                    const size_t row = base + min(r[k], rows - 1);
+                    load_now(a.part_ml + 2 * row, ml[u][k]);
+                    load_now(a.part_acc + row * D + lane * DPL, x[u][k]);
                 }
             }
 #pragma unroll
-            for (int u = 0; u < kMergeBatch; ++u) {
-                if (mc[u] == -INFINITY) continue;
-                const float mn = fmaxf(M, mc[u]);
-                const float al = ex2_approx(M - mn);   // 0 while M = -inf
-                const float wc = ex2_approx(mc[u] - mn);
-                M = mn;
-                L = fmaf(wc, lc[u], L * al);
+            for (int k = 0; k < R; ++k) {
+                float mn = M[k];
 #pragma unroll
-                for (int i = 0; i < DPL; ++i) A[i] = fmaf(wc, x[u][i], A[i] * al);
+                for (int u = 0; u < kMergeBatch; ++u)
+                    if (n0 + u * W < count) mn = fmaxf(mn, ml[u][k].x);
+                const float ref = mn == -INFINITY ? 0.f : mn;
+                const float al = ex2_approx(M[k] - ref);   // 0 while M = -inf
+                M[k] = mn;
+                L[k] *= al;
+#pragma unroll
+                for (int i = 0; i < DPL; ++i) A[k][i] *= al;
+#pragma unroll
+                for (int u = 0; u < kMergeBatch; ++u) {
+                    if (n0 + u * W < count) {
+                        const float w = ex2_approx(ml[u][k].x - ref);
+                        L[k] = fmaf(w, ml[u][k].y, L[k]);
+#pragma unroll
+                        for (int i = 0; i < DPL; ++i) A[k][i] = fmaf(w, x[u][k][i], A[k][i]);
+                    }
+                }
             }
         }
         if constexpr (W > 1) {
-            if (r0 > (int)blockIdx.y * per) __syncthreads();   // the last row's have been read
+            static_assert(R == 1, "a row a warp");
+            __syncthreads();   // the unit's before has been read
 #pragma unroll
-            for (int i = 0; i < DPL; ++i) s_acc[wi][lane * DPL + i] = A[i];
-            if (lane == 0) s_ml[wi] = make_float2(M, L);
+            for (int i = 0; i < DPL; ++i) s_acc[warp][lane * DPL + i] = A[0][i];
+            if (lane == 0) s_ml[warp] = make_float2(M[0], L[0]);
             __syncthreads();
             if (wi != 0) continue;
-            M = -INFINITY;
+            M[0] = -INFINITY;
 #pragma unroll
-            for (int k = 0; k < W; ++k) M = fmaxf(M, s_ml[k].x);
-            L = 0.f;
+            for (int k = 0; k < W; ++k) M[0] = fmaxf(M[0], s_ml[warp + k].x);
+            L[0] = 0.f;
 #pragma unroll
-            for (int i = 0; i < DPL; ++i) A[i] = 0.f;
+            for (int i = 0; i < DPL; ++i) A[0][i] = 0.f;
 #pragma unroll
             for (int k = 0; k < W; ++k) {
-                const float2 ml = s_ml[k];
-                const float wk = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
-                L = fmaf(wk, ml.y, L);
+                const float2 ml = s_ml[warp + k];
+                const float wk = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M[0]);
+                L[0] = fmaf(wk, ml.y, L[0]);
 #pragma unroll
-                for (int i = 0; i < DPL; ++i) A[i] = fmaf(wk, s_acc[k][lane * DPL + i], A[i]);
+                for (int i = 0; i < DPL; ++i) A[0][i] = fmaf(wk, s_acc[warp + k][lane * DPL + i], A[0][i]);
             }
         }
-        const float inv = L == 0.f ? 0.f : 1.f / L;
-        const size_t row = (size_t)(p.q0 + tok) * a.H + p.h * G + r % G;
-        uint16_t* out = static_cast<uint16_t*>(a.o) + row * D + lane * DPL;
 #pragma unroll
-        for (int i = 0; i < DPL; i += 2)
-            *reinterpret_cast<uint32_t*>(out + i) = pack_bf16x2(A[i] * inv, A[i + 1] * inv);
-        if (lane == 0) a.lse[row] = L == 0.f ? -INFINITY : (M + __log2f(L)) * kLn2;
+        for (int k = 0; k < R; ++k) {
+            const int tok = p.tok0 + r[k] / G;
+            if (r[k] >= rows || tok >= p.n) continue;
+            const float inv = L[k] == 0.f ? 0.f : 1.f / L[k];
+            const size_t row = (size_t)(p.q0 + tok) * a.H + p.h * G + r[k] % G;
+            uint16_t* out = static_cast<uint16_t*>(a.o) + row * D + lane * DPL;
+#pragma unroll
+            for (int i = 0; i < DPL; i += 2)
+                *reinterpret_cast<uint32_t*>(out + i) = pack_bf16x2(A[k][i] * inv, A[k][i + 1] * inv);
+            if (lane == 0) a.lse[row] = L[k] == 0.f ? -INFINITY : (M[k] + __log2f(L[k])) * kLn2;
+        }
     }
 }
 
@@ -903,11 +970,11 @@ cudaError_t launch_d(const PagedTcArgs& a, int sm_count, cudaStream_t stream) {
     cfg.numAttrs = 1;
     if ((e = cudaLaunchKernelEx(&cfg, kern, a.tm_q, a.tm_k, a.tm_v, a)) != cudaSuccess) return e;
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    const int rows = 2 * a.tt * (a.H / a.Hkv);
-    cfg.gridDim = dim3((unsigned)sm_count, (unsigned)(FEW ? 1 : (rows + 15) / 16));
+    constexpr int kW = FEW ? 8 : 1, kR = FEW ? 1 : 2;
+    cfg.gridDim = dim3((unsigned)((FEW ? kMergeBlocksFew : kMergeBlocks) * sm_count));
     cfg.blockDim = dim3(kMergeThreads);
     cfg.dynamicSmemBytes = 0;
-    e = cudaLaunchKernelEx(&cfg, paged_tc_merge_kernel<D / 32, FEW ? 8 : 1>, a, sm_count);
+    e = cudaLaunchKernelEx(&cfg, paged_tc_merge_kernel<D / 32, kW, kR>, a, sm_count);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -921,6 +988,7 @@ int paged_tc_tokens(int G, int max_q) {
 
 cudaError_t launch_paged_tc(const PagedTcArgs& a, int sm_count, cudaStream_t stream) {
     const bool few = a.tt * (a.H / a.Hkv) <= kFewRows;
+    sm_count = sm_count < kMergeThreads ? sm_count : kMergeThreads;   // the merge looks at a share per thread
     if (a.D == 64) return few ? launch_d<64, true>(a, sm_count, stream) : launch_d<64, false>(a, sm_count, stream);
     return few ? launch_d<128, true>(a, sm_count, stream) : launch_d<128, false>(a, sm_count, stream);
 }
