@@ -861,12 +861,20 @@ __global__ void __launch_bounds__(kMergeThreads, W > 1 ? kMergeBlocksFew : kMerg
     const int G = a.H / a.Hkv;
     const int rows = 2 * a.tt * G;
     const int slices = (rows + kRows - 1) / kRows;
-    for (int unit = (int)blockIdx.x; unit < items * slices; unit += (int)gridDim.x) {
-        const Split p = s_item[unit % items];
+    // r / G of a row (exact for r < 600, G <= 128): the divisions were half of the kernel's instructions
+    const unsigned over_g = (1u << 20) / (unsigned)G + 1u;
+    auto token_of = [&](int r) { return (int)(((unsigned)r * over_g) >> 20); };
+    // unit: slice u of item k, the items' first slices first
+    int u0 = items > 0 ? (int)blockIdx.x / items : slices, k0 = (int)blockIdx.x - u0 * items;
+    auto advance = [&] {
+        for (k0 += (int)gridDim.x; k0 >= items && u0 < slices; k0 -= items) ++u0;
+    };
+    for (; u0 < slices; advance()) {
+        const Split p = s_item[k0];
         const int* slot = s_slot + p.at;
-        const int count = s_item[unit % items + 1].at - p.at;
-        const int row0 = unit / items * kRows;
-        if (p.tok0 + row0 / G >= p.n) continue;
+        const int count = s_item[k0 + 1].at - p.at;
+        const int row0 = u0 * kRows;
+        if (p.tok0 + token_of(row0) >= p.n) continue;
         const int wi = warp % W;
         float M[R], L[R], A[R][DPL];
         int r[R];
@@ -939,10 +947,11 @@ __global__ void __launch_bounds__(kMergeThreads, W > 1 ? kMergeBlocksFew : kMerg
         }
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            const int tok = p.tok0 + r[k] / G;
+            const int t = token_of(r[k]);
+            const int tok = p.tok0 + t;
             if (r[k] >= rows || tok >= p.n) continue;
             const float inv = L[k] == 0.f ? 0.f : 1.f / L[k];
-            const size_t row = (size_t)(p.q0 + tok) * a.H + p.h * G + r[k] % G;
+            const size_t row = (size_t)(p.q0 + tok) * a.H + p.h * G + r[k] - t * G;
             uint16_t* out = static_cast<uint16_t*>(a.o) + row * D + lane * DPL;
 #pragma unroll
             for (int i = 0; i < DPL; i += 2)
