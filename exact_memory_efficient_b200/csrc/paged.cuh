@@ -35,13 +35,17 @@ __device__ __forceinline__ Seq load_seq(const PagedBatch& s, int b) {
     return r;
 }
 
-// Page of the sequence's keys [i << page_shift, (i + 1) << page_shift), i < max_pages.
-__device__ __forceinline__ int load_page(const PagedBatch& s, int b, int i) {
-    const int p = s.page_table[(size_t)b * s.max_pages + i];
-    if ((unsigned)p < (unsigned)s.num_pages) return p;
+// Entry of the sequence's keys [i << page_shift, (i + 1) << page_shift), i < max_pages,
+// and the page that it names.  Apart where the entry is asked for ahead of its use.
+__device__ __forceinline__ int page_entry(const PagedBatch& s, int b, int i) {
+    return s.page_table[(size_t)b * s.max_pages + i];
+}
+__device__ __forceinline__ int page_of(const PagedBatch& s, int entry) {
+    if ((unsigned)entry < (unsigned)s.num_pages) return entry;
     flag_bad_page();
     return 0;
 }
+__device__ __forceinline__ int load_page(const PagedBatch& s, int b, int i) { return page_of(s, page_entry(s, b, i)); }
 
 // A tile of 128 keys of bf16 pages in shared memory, as one TMA box per page
 // lays it out: groups of 8 keys, in a group the blocks of 64 head dims, in a
@@ -101,7 +105,15 @@ __device__ __forceinline__ int find_row(const PagedBatch& s, int t) {
 // The costs of all sequences as one line: calls locate(b, before, cost, W) for
 // every b, with the sum of the costs in front of b and of all.  All THREADS
 // threads of the block call it; a thread's cost(b) and locate(b, ...) calls
-// follow one another, so that cost() may leave what locate() needs.
+// follow one another, so that cost() may leave what locate() needs.  What locate()
+// writes is seen after the block's next barrier.
+// x / y, and the border of share i of n, of sizes that most often fit 32 bits (a
+// division of 64-bit numbers takes some 150 cycles, and shares are found before any work)
+__device__ __forceinline__ long long divide(long long x, long long y) {
+    return (unsigned long long)(x | y) >> 32 ? x / y : (long long)((unsigned)x / (unsigned)y);
+}
+__device__ __forceinline__ long long share_begin(long long W, unsigned i, unsigned n) { return divide(W * i, n); }
+
 template <int THREADS, typename Cost, typename Locate>
 __device__ __forceinline__ void lay_out_costs(int B, long long (&warp_sum)[THREADS / 32], Cost&& cost, Locate&& locate) {
     const int tid = (int)threadIdx.x;
@@ -126,6 +138,19 @@ __device__ __forceinline__ void lay_out_costs(int B, long long (&warp_sum)[THREA
         *all = total;
         return before + upto - x;
     };
+    if (B <= 32) {   // one warp's work: no exchange between warps
+        if (warp != 0) return;
+        const long long mine = (int)lane < B ? cost((int)lane) : 0;
+        long long upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= (unsigned)o) upto += y;
+        }
+        const long long W = __shfl_sync(0xffffffffu, upto, 31);
+        if ((int)lane < B) locate((int)lane, upto - mine, mine, W);
+        return;
+    }
     long long W = 0, mine = 0, before = 0;
     for (int b0 = 0; b0 < B; b0 += THREADS) {
         long long all;

@@ -204,16 +204,16 @@ __device__ __forceinline__ void find_share(const PagedTcArgs& a, Barriers* bars)
         return sum * a.Hkv;
     };
     auto locate = [&](int b, long long before, long long sum, long long W) {
-        const long long w0 = W * blockIdx.x / gridDim.x, w1 = W * (blockIdx.x + 1) / gridDim.x;
+        const long long w0 = share_begin(W, blockIdx.x, gridDim.x), w1 = share_begin(W, blockIdx.x + 1, gridDim.x);
         if (w0 < before || w0 >= before + sum || w1 <= w0) return;
         const int items = items_of(sq, a.tt);   // sq is b's since cost(b)
-        const long long per_head = sum / a.Hkv;
+        const long long per_head = divide(sum, a.Hkv);
         long long x = w0 - before;
         Barriers::Share& at = bars->share;
         at.cost = w1 - w0;
         at.sq = sq;
         at.b = b;
-        at.h = (int)(x / per_head);
+        at.h = (int)divide(x, per_head);
         x -= at.h * per_head;
         int i = 0;
         for (; i + 1 < items; ++i) {
@@ -305,8 +305,14 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         };
         const int slot = 2 * (int)blockIdx.x;           // the CTA's workspace slots
         if (lane == 0) a.parts[slot].n_kv = a.parts[slot + 1].n_kv = 0;     // no part yet
+        // the lane's entry of the page table for key tile j, asked for a tile ahead
+        auto look_up = [&](int j) {
+            const int key = j * kTile + my_row;
+            return mine && key < w.sq.L ? page_entry(a.s, w.b, key >> shift) : 0;
+        };
         for (w.begin(a.s, bars->share, a.Hkv, tt); ok && !w.done(); w.next(a.s, a.Hkv, tt), ++li) {
             const int n_qt = w.two(tt) ? 2 : 1;
+            int entry = look_up(w.t0);
             if (li > 0 && !(ok = wait(&bars->q_empty, (li - 1) & 1))) break;
             if (lane == 0) {
                 if (!w.whole()) {
@@ -328,10 +334,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             }
             q_asked = li + 1;
             for (int j = w.t0; ok && j < w.t1; ++j) {
-                // the lane's page, looked up while the stage drains
                 const int key = j * kTile + my_row;
                 int z = outside;
-                if (mine && key < w.sq.L) z = load_page(a.s, w.b, key >> shift) * a.Hkv + w.h;
+                if (mine && key < w.sq.L) z = page_of(a.s, entry) * a.Hkv + w.h;
+                if (j + 1 < w.t1) entry = look_up(j + 1);
                 const int group = (key & ((1 << shift) - 1)) >> 3;
 #pragma unroll
                 for (int v = 0; v < 2; ++v, ++c_glob) {

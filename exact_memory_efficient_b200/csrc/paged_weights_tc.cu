@@ -154,18 +154,18 @@ __device__ __forceinline__ void find_share(const PagedWeightsTcArgs& a, Barriers
         return sum * a.Hkv;
     };
     auto locate = [&](int b, long long before, long long sum, long long W) {
-        const long long w0 = W * blockIdx.x / gridDim.x, w1 = W * (blockIdx.x + 1) / gridDim.x;
+        const long long w0 = share_begin(W, blockIdx.x, gridDim.x), w1 = share_begin(W, blockIdx.x + 1, gridDim.x);
         if (w0 < before || w0 >= before + sum || w1 <= w0) return;
         const int items = items_of(sq), full = full_items(sq), nq = q_tiles(sq, a.tt);   // sq is b's since cost(b)
-        const long long per_head = sum / a.Hkv;
+        const long long per_head = divide(sum, a.Hkv);
         long long x = w0 - before;
         Barriers::Share& at = bars->share;
         at.units = w1 - w0;
         at.sq = sq;
         at.b = b;
-        at.h = (int)(x / per_head);
+        at.h = (int)divide(x, per_head);
         x -= at.h * per_head;
-        int i = (int)min((long long)full, x / nq);
+        int i = (int)min((long long)full, divide(x, nq));
         x -= (long long)i * nq;
         for (; i >= full && i + 1 < items; ++i) {
             const int n = units_of(sq, a.tt, i);
