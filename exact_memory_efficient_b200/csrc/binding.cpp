@@ -73,7 +73,14 @@ float number(const char* where, const char* name, PyObject* o) {
     return (float)x;
 }
 
-bool truth(PyObject* o) { return PyObject_IsTrue(o) == 1; }
+bool truth(const char* where, const char* name, PyObject* o) {
+    const int x = PyObject_IsTrue(o);
+    if (x < 0) {
+        PyErr_Clear();
+        bad(where, std::string(name) + " must be true or false");
+    }
+    return x != 0;
+}
 
 mea_dtype_t dtype_of(const at::Tensor& t) {
     if (t.scalar_type() == at::kFloat) return MEA_DTYPE_F32;
@@ -117,10 +124,18 @@ struct Stream {
         PyObject* h = PyLong_Check(o) ? Py_NewRef(o) : PyObject_GetAttrString(o, "cuda_stream");
         if (h != nullptr) handle = PyLong_AsVoidPtr(h);
         Py_XDECREF(h);
+        long index = dev.index();
+        if (!PyErr_Occurred() && !PyLong_Check(o)) {
+            PyObject* at = PyObject_GetAttrString(o, "device_index");
+            if (at != nullptr) index = PyLong_AsLong(at);
+            else PyErr_Clear();   // an object of another library with a handle only
+            Py_XDECREF(at);
+        }
         if (PyErr_Occurred()) {
             PyErr_Clear();
             bad(where, "stream must be a CUDA stream or its handle");
         }
+        if (index != dev.index()) bad(where, "stream is not on the device of the first tensor");
     }
     // Outputs and scratch belong to the call's stream, so that the allocator does
     // not hand their memory on while the call may still run.
@@ -223,13 +238,13 @@ PyObject* rope(PyObject* const* p) {
         !(per_batch && positions.size(0) == B && positions.size(1) == N))
         bad(w, "positions must be [N] or [B, N]");
     const mea_dtype_t dt = dtype_of(x);
+    const int layout = integer(w, "layout", p[4]), inverse = truth(w, "inverse", p[6]);
+    const float mscale = number(w, "mscale", p[5]);
     const Device d(w, x);
     d.dense("x", x, x.scalar_type());
     d.dense("y", y, x.scalar_type());
     d.dense("positions", positions, at::kInt);
     d.dense("freq", freq, at::kDouble);
-    const int layout = integer(w, "layout", p[4]), inverse = truth(p[6]);
-    const float mscale = number(w, "mscale", p[5]);
     const Stream s(w, p[7], d.dev);
     if (!y.defined()) y = s.empty(x.sizes(), x.scalar_type());
     const int b = as_int(w, B), h = as_int(w, x.size(1)), n = as_int(w, N), D = as_int(w, x.size(3)),
@@ -247,7 +262,7 @@ PyObject* append(PyObject* const* p) {
     const char* w = "mea_paged_append";
     const at::Tensor q = tensor(w, "q", p[0], true);
     at::Tensor q_out = tensor(w, "q_out", p[1], true);
-    const bool make = truth(p[2]);
+    const bool make = p[2] == Py_True;
     const at::Tensor k = tensor(w, "k", p[3]), v = tensor(w, "v", p[4]), kc = tensor(w, "k_cache", p[5]),
                      vc = tensor(w, "v_cache", p[6]), wt = tensor(w, "weights", p[7], true),
                      cu = tensor(w, "cu_q", p[8]), kv = tensor(w, "kv_len", p[9]), tab = tensor(w, "page_table", p[10]),
@@ -304,7 +319,7 @@ PyObject* attend(PyObject* const* p) {
     const char* w = "mea_attn_paged";
     const at::Tensor q = tensor(w, "q", p[0]), kc = tensor(w, "k_cache", p[1]), vc = tensor(w, "v_cache", p[2]);
     at::Tensor o = tensor(w, "o", p[3], true), lse = tensor(w, "lse", p[4], true), ws = tensor(w, "workspace", p[12], true);
-    const bool make = truth(p[5]);
+    const bool make = p[5] == Py_True;
     const at::Tensor cu = tensor(w, "cu_q", p[6]), kv = tensor(w, "kv_len", p[7]), tab = tensor(w, "page_table", p[8]);
     const int max_q = integer(w, "max_q", p[9]), max_kv = integer(w, "max_kv", p[10]);
     const Cache c(w, kc, vc, at::Tensor());
@@ -348,7 +363,7 @@ PyObject* weigh(PyObject* const* p) {
     const char* w = "mea_attn_paged_weights";
     const at::Tensor q = tensor(w, "q", p[0]), lse = tensor(w, "lse", p[1]), kc = tensor(w, "k_cache", p[2]),
                      wt = tensor(w, "weights", p[3]);
-    const bool make = truth(p[4]);
+    const bool make = p[4] == Py_True;
     const at::Tensor cu = tensor(w, "cu_q", p[5]), kv = tensor(w, "kv_len", p[6]), tab = tensor(w, "page_table", p[7]);
     const int max_q = integer(w, "max_q", p[8]), max_kv = integer(w, "max_kv", p[9]);
     at::Tensor ws = tensor(w, "workspace", p[11], true);

@@ -201,3 +201,23 @@ def test_binding_refuses_cpu_tensors_and_shapes():
     x, pos, fr = torch.zeros(1, 2, 8, 64, dtype=bf), torch.zeros(8, dtype=i32), torch.zeros(8, dtype=torch.float64)
     for bad in ((x, x, pos, fr), (x, x[:, :1], pos, fr), (x, x, pos[:3], fr), (x[0], x[0], pos, fr), (x, x, pos, fr[None])):
         refused(m.mea_rope, *bad)
+
+
+def test_binding_refuses_arguments_of_other_types(lib):
+    x, pos, freq = torch.zeros(1, 2, 8, 64), torch.zeros(8, dtype=torch.int32), torch.zeros(32, dtype=torch.float64)
+    q, kc = torch.zeros(4, 4, 64), torch.zeros(8, 2, 16, 64)
+    cu, kv, table = (torch.zeros(n, dtype=torch.int32) for n in ((3,), (2,), (2, 4)))
+
+    def refused(word, f, *args, **kw):
+        with pytest.raises(m.MeaError) as e:
+            f(*args, **kw)
+        assert e.value.status == INVALID and word in str(e.value)
+
+    refused("x must be a tensor", m.rope, x.numpy(), pos, freq)
+    refused("freq must be a tensor", m.rope, x, pos, None)
+    refused("inverse", m.rope, x, pos, freq, inverse=np.ones(2))
+    refused("mscale", m.rope, x, pos, freq, mscale="1")
+    refused("max_q", m.attention_paged, q, kc, kc, cu, kv, table, 1.5, 64)
+    refused("max_q", m.attention_paged, q, kc, kc, cu, kv, table, 2**40, 64)
+    refused("max_kv", m.attention_paged, q, kc, kc, cu, kv, table, 1, None)
+    refused("n_keep", m.paged_evict, kc, kc, torch.zeros(8, 2, 16), table, kv, table, 0, 0)

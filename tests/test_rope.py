@@ -1,5 +1,8 @@
 """mea_rope against the fp64 definition (GPU)."""
 
+import threading
+from types import SimpleNamespace
+
 import numpy as np
 import pytest
 import torch
@@ -61,6 +64,48 @@ def test_in_place_equals_out_of_place_and_other_stream():
     assert torch.equal(y, want)
     m.mea_rope(x, x, pos, freq)
     assert torch.equal(x, want)
+
+
+def test_streams_of_the_binding():
+    """None, a torch stream and its handle name the same stream; another device's and other objects are refused."""
+    x = torch.randn(2, 8, 300, 128, device="cuda").to(BF)
+    pos = torch.arange(300, dtype=torch.int32, device="cuda")
+    freq = m.mea_rope_frequencies(96).cuda()
+    want = m.rope(x, pos, freq)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    y = m.rope(x, pos, freq, stream=s.cuda_stream)
+    s.synchronize()
+    assert torch.equal(y, want)
+    y = m.rope(x, pos, freq, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)
+    for bad in (SimpleNamespace(cuda_stream=s.cuda_stream, device_index=1), object(), "0", 2.5):
+        with pytest.raises(m.MeaError) as e:
+            m.rope(x, pos, freq, stream=bad)
+        assert e.value.status == m.MEA_ERR_INVALID_ARG and "stream" in str(e.value)
+
+
+def test_calls_from_two_threads():
+    xs = [torch.randn(2, 4, 200, 64, device="cuda") for _ in range(2)]
+    pos = torch.arange(200, dtype=torch.int32, device="cuda")
+    freq = m.mea_rope_frequencies(64).cuda()
+    want = [m.rope(x, pos, freq) for x in xs]
+    torch.cuda.synchronize()
+    out = [None, None]
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(200):
+                out[i] = m.rope(xs[i], pos, freq)
+            torch.cuda.current_stream().synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
 
 
 @pytest.mark.parametrize("interleaved", [False, True])
