@@ -84,6 +84,17 @@ def test_attention_f32(counts, lens, H, Hkv, D, page):
     check(bt, run(bt))
 
 
+@pytest.mark.parametrize("counts,lens,H,Hkv,D,page", [
+    ([1], [19000], 4, 1, 128, 64), ([70], [19000], 2, 1, 64, 16), ([3, 1], [9500, 9400], 5, 1, 64, 128),
+    ([1] * 33, [i * 37 % 300 for i in range(33)], 4, 2, 128, 16),
+    ([i % 3 for i in range(330)], [i * 13 % 60 for i in range(330)], 2, 1, 64, 16),
+])
+def test_many_parts_and_many_sequences(counts, lens, H, Hkv, D, page):
+    """An item cut into about as many parts as there are SMs; batches beyond a warp's and a block's threads."""
+    bt = Batch(counts, lens, H, Hkv, D, page, BF, seed=21)
+    check(bt, run(bt))
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("counts,lens", [([4, 1, 3], [2, 0, 50]), ([40, 300], [0, 170]), ([1, 1], [0, 3])])
 def test_rows_that_see_no_key(dtype, counts, lens):

@@ -53,6 +53,17 @@ def test_weights(dtype, counts, lens, H, Hkv, D, page):
     check(bt, lse, run(bt, lse))
 
 
+@pytest.mark.parametrize("counts,lens,H,Hkv,D,page", [
+    ([1500], [1500], 2, 1, 64, 16), ([2000], [2040], 4, 1, 128, 64), ([1] * 33, [i * 37 % 300 for i in range(33)], 4, 2, 128, 16),
+    ([i % 3 for i in range(610)], [i * 13 % 60 for i in range(610)], 2, 1, 64, 16),
+])
+def test_many_parts_and_many_sequences(counts, lens, H, Hkv, D, page):
+    """An item's units spread over tens of SMs; batches beyond a warp's and a block's threads."""
+    bt = Batch(counts, lens, H, Hkv, D, page, BF, seed=22)
+    lse = exact_lse(bt)
+    check(bt, lse, run(bt, lse))
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_rows_that_see_nothing_add_nothing(dtype):
     bt = Batch([5, 40, 1], [2, 17, 0], 4, 2, 64, 16, dtype, seed=3)
