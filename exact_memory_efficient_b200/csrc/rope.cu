@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a, in
 
 // Heads per thread: as many as leave every SM some 768 threads (the sines are
 // formed once per slice), at most 16: rope of 1 x 16 x 16384 x 128 bf16 takes
-// 21.5 us (6.2 TB/s), with 1,024 threads and at most 8 heads 22.4, with at most 4
+// 21.5 us, with 1,024 threads and at most 8 heads 22.4, with at most 4
 // heads 25.4.
 int heads_per_slice(long long threads_per_head, int H, int sm_count) {
     const long long per = threads_per_head * H / ((long long)sm_count * 768);
