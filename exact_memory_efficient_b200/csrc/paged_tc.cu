@@ -426,6 +426,9 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 // A slot's first P V overwrites its O.  Its own epilogue of the
                 // item before is over when its softmax hands over P; after a
                 // single item the other slot's epilogue has read it as well.
+                // The parity names the item before: the wait must come ahead of
+                // the o_final that lets slot t ^ 1 finish this item, or that slot
+                // may arrive once more and the parity is that of the item after.
                 auto o_is_free = [&](int t) -> bool {
                     return !prev_single || mbar_wait(&bars->o_free[t ^ 1], (li - 1) & 1, abort_flag);
                 };
@@ -481,6 +484,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                             if (j == 0 && !(ok = o_is_free(0))) break;
                             if (!(ok = pv_halves(0, cnt0 & 1, v_off, acc0))) break;
                             ++cnt0;
+                            // slot 0 has handed over a P of this item: no wait, but ahead of its o_final
+                            if (j == 0 && !(ok = o_is_free(1))) break;
                             if (j == n0 - 1) mma_commit(&bars->o_final[0]);
                         }
                         if (more) {
@@ -491,7 +496,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                                 mma_commit(&bars->s_full[0]);
                             }
                         }
-                        if (j == 0 && !(ok = o_is_free(1))) break;
+                        if (j == 0 && n0 == 0 && !(ok = o_is_free(1))) break;   // slot 0's o_final is the item's end
                         if (!(ok = pv_halves(1, cnt1 & 1, v_off, acc0))) break;
                         ++cnt1;
                         mma_commit(&bars->empty[v_stage]);
