@@ -68,21 +68,35 @@ constexpr float kRescaleThreshold = 8.0f;
 constexpr float kNoKey = -1e30f;  // reference maximum of a row that has seen no key (finite: no inf - inf)
 constexpr unsigned kIdescNegateA = 1u << 13;
 
-// FEW: at most kFewRows rows per query tile (decode).  Their Q takes 2 KB per 64
+// FEW: at most kFewRows rows per query tile (decode).  Their Q takes 4 KB per 64
 // head dims instead of 16 KB (the MMA's other rows read whatever follows, and a
 // row of S depends on its own row of Q alone), and the space goes to the ring:
 // six tiles in flight instead of four.
+//
+// Rounding of P.  P V takes bf16 operands.  With few rows a probability is the sum
+// of two bf16 terms, p and what rounding p leaves: at most 2^-16 p is lost, as little
+// as the fp32 decode of contiguous keys (decode.cu) would notice in a bf16 result.
+// The terms are two rows of the same MMA: Q is loaded twice, 16 rows apart, the
+// lanes of a row and of its copy have the same S, form 32 of every 64 probabilities
+// each and exchange the terms; the two rows of O are added at the item's end (ragged
+// decode of 16 over 8191 keys, 32 over 8 heads: 65.2 us with one term, 64.7 so; with
+// every lane on all of its row's columns 74.5, and as a second MMA 82).
+// Larger tiles have no rows to spare: there P is rounded to bf16 once, at most 2^-8 p
+// of each value with either sign, as in the forward kernels; a second MMA for the
+// rest takes 3 chunks of 97 to 250 tokens over 16384 keys from 158 to 218 us, 4
+// prompts of 4096 from 326 to 454.  The sums take p in fp32 in both.
 constexpr int kFewRows = 16;
 
 template <int D, bool FEW>
 struct Cfg {
-    static constexpr int kQBox = FEW ? kFewRows * 128 : 128 * 128;   // 64 head dims of a query tile
+    static constexpr int kCopies = FEW ? 2 : 1;                      // of every query row
+    static constexpr int kQBox = FEW ? kCopies * kFewRows * 128 : 128 * 128;   // 64 head dims of a query tile
     static constexpr int kQBytes = D / 64 * kQBox;
     static constexpr int kTileBytes = kTile * D * 2;     // K or V tile
     static constexpr int kStages = D == 64 ? (FEW ? 8 : 6) : (FEW ? 6 : 4);
     static constexpr int kSmemData = (2 * kQBytes + kStages * kTileBytes + 1023) / 1024 * 1024;
     static constexpr int kMergeBytes = 2 * kTile * 2 * 4;   // both slots' (m, l) per row
-    static constexpr int kStageBytes = 8 * 2048;            // epilogue: 32 rows x 64 bytes per warp
+    static constexpr int kStageBytes = (FEW ? 2 : 8) * 2048;   // epilogue: 32 rows x 64 bytes per warp with rows
     static constexpr int kSmemBytes = kSmemData + kMergeBytes + kStageBytes + 1024 /*barriers*/ + 1024 /*alignment*/;
     static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
@@ -328,11 +342,11 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     p.q0 = w.sq.q0;
                     p.n = w.sq.n;
                 }
-                mbar_arrive_expect_tx(&bars->q_full, (unsigned)(n_qt * G * tt * D * 2));
+                mbar_arrive_expect_tx(&bars->q_full, (unsigned)(n_qt * C::kCopies * G * tt * D * 2));
                 for (int t = 0; t < n_qt; ++t)
-                    for (int x = 0; x < D / 64; ++x)
-                        tma_load_3d(sQ + t * C::kQBytes + x * C::kQBox, &tm_q, &bars->q_full, x * 64, w.h * G,
-                                    w.sq.q0 + (2 * w.i + t) * tt);
+                    for (int x = 0; x < D / 64 * C::kCopies; ++x)
+                        tma_load_3d(sQ + t * C::kQBytes + x * (C::kQBox / C::kCopies), &tm_q, &bars->q_full,
+                                    x / C::kCopies * 64, w.h * G, w.sq.q0 + (2 * w.i + t) * tt);
             }
             q_asked = li + 1;
             for (int j = w.t0; ok && j < w.t1; ++j) {
@@ -538,8 +552,11 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         const unsigned tO = tmem + lane_off + (t ? 384u : 256u);
         // S carries the sign; a scale of 0 must not meet the mask's infinity
         const float c_log2 = fmaxf(fabsf(a.scale) * kLog2e, 1e-37f);
-        const int tok_r = r / G;               // token of row r in its query tile
-        const int g_r = r - tok_r * G;
+        // row of the query tile; with few rows lanes 16-31 hold the copies of rows 0-15
+        const int q_r = FEW && sub == 0 ? r % kFewRows : r;
+        const bool copy = FEW && r >= kFewRows;
+        const int tok_r = q_r / G;             // its token in the query tile
+        const int g_r = q_r - tok_r * G;
         const int page = 1 << a.s.page_shift;
         // a wait that gives up does so for the whole warp: the code behind it is collective
         auto wait_all = [&](uint64_t* bar, unsigned parity) -> bool {
@@ -561,7 +578,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             // own its one tile and key tiles t, t+2, ...
             const int n_mine = single ? (cnt + 1 - t) / 2 : (t ? cnt : n0);
             const int tok = w.tok0 + (single ? 0 : t * tt) + tok_r;
-            const bool valid = tok_r < tt && tok < w.n;
+            const bool valid = !copy && tok_r < tt && tok < w.n;
             const bool live = __any_sync(0xffffffffu, valid);   // rows of other lanes never meet this warp's
             // keys the row sees, from the part's first key on
             const int lim = max(0, w.seen + min(tok, w.n - 1) + 1) - w.base;
@@ -599,25 +616,37 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     mbar_arrive(&bars->p_ready[t]);
                     continue;
                 }
-                uint32_t sr[kTile];
+                // the lane's scores: with few rows 32 of every 64, the copy's lane has the others
+                constexpr int kOwn = FEW ? kTile / 2 : kTile;
+                uint32_t sr[kOwn];
+                if constexpr (FEW) {
+                    uint32_t all[kTile];
 #pragma unroll
-                for (int c0 = 0; c0 < kTile; c0 += 32) tmem_ld32(tS + c0, *reinterpret_cast<uint32_t(*)[32]>(&sr[c0]));
-                tmem_wait_ld();
+                    for (int c0 = 0; c0 < kTile; c0 += 32) tmem_ld32(tS + c0, *reinterpret_cast<uint32_t(*)[32]>(&all[c0]));
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int c = 0; c < kOwn; ++c) sr[c] = copy ? all[c + (c & 32) + 32] : all[c + (c & 32)];
+                } else {
+#pragma unroll
+                    for (int c0 = 0; c0 < kTile; c0 += 32) tmem_ld32(tS + c0, *reinterpret_cast<uint32_t(*)[32]>(&sr[c0]));
+                    tmem_wait_ld();
+                }
                 if (j >= mask_j) {
-                    const int nvalid = lim - j * kTile;
+                    const int nvalid = lim - j * kTile - (copy ? 32 : 0);
 #pragma unroll
-                    for (int c = 0; c < kTile; ++c)
-                        if (c >= nvalid) sr[c] = __float_as_uint(-INFINITY);
+                    for (int c = 0; c < kOwn; ++c)
+                        if ((FEW ? c + (c & 32) : c) >= nvalid) sr[c] = __float_as_uint(-INFINITY);
                 }
                 float mxa[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) mxa[i] = fmaxf(__uint_as_float(sr[i]), __uint_as_float(sr[8 + i]));
 #pragma unroll
-                for (int c = 16; c < kTile; c += 16)
+                for (int c = 16; c < kOwn; c += 16)
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         mxa[i] = fmax3(mxa[i], __uint_as_float(sr[c + i]), __uint_as_float(sr[c + 8 + i]));
-                const float mx = fmaxf(fmax3(mxa[0], mxa[1], mxa[2]), fmax3(fmax3(mxa[3], mxa[4], mxa[5]), mxa[6], mxa[7]));
+                float mx = fmaxf(fmax3(mxa[0], mxa[1], mxa[2]), fmax3(fmax3(mxa[3], mxa[4], mxa[5]), mxa[6], mxa[7]));
+                if constexpr (FEW) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, kFewRows));
                 const float m_blk = fmaxf(mx * c_log2, kNoKey);
                 float alpha = 1.f;
                 bool rescale = false;
@@ -634,8 +663,9 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
 #pragma unroll
                 for (int i = 0; i < 8; ++i) rsa[i] = 0.f;
 #pragma unroll
-                for (int c0 = 0; c0 < kTile; c0 += 32) {
+                for (int c0 = 0; c0 < kOwn; c0 += 32) {
                     uint32_t pk[16];
+                    [[maybe_unused]] uint32_t rest[16];
 #pragma unroll
                     for (int c = 0; c < 32; c += 2) {
                         float p0 = -m_ref, p1 = -m_ref;
@@ -644,9 +674,25 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                         p1 = ex2_approx(p1);
                         rsa[(c / 2) & 7] += p0 + p1;
                         pk[c / 2] = pack_bf16x2(p0, p1);
+                        if constexpr (FEW)
+                            rest[c / 2] = pack_bf16x2(p0 - __uint_as_float(pk[c / 2] << 16),
+                                                      p1 - __uint_as_float(pk[c / 2] & 0xffff0000u));
                     }
-                    tmem_st16(tS + c0 / 2, pk);
-                    if (c0 == kTile / 2 - 32 && !rescale) {
+                    if constexpr (FEW) {
+                        // the row's lane stores the first terms, the copy's lane the second ones
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) {
+                            const uint32_t below = __shfl_up_sync(0xffffffffu, rest[c], kFewRows);
+                            const uint32_t above = __shfl_down_sync(0xffffffffu, pk[c], kFewRows);
+                            pk[c] = copy ? below : pk[c];
+                            rest[c] = copy ? rest[c] : above;
+                        }
+                        tmem_st16(tS + c0, pk);
+                        tmem_st16(tS + c0 + 16, rest);
+                    } else {
+                        tmem_st16(tS + c0 / 2, pk);
+                    }
+                    if (c0 == kOwn / 2 - 32 && !rescale) {
                         tmem_wait_st();
                         tc_fence_before();
                         mbar_arrive(&bars->p_half[t]);
@@ -673,6 +719,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             }
             if (!ok) break;
             ring += 2 * cnt;
+            if constexpr (FEW) l += __shfl_xor_sync(0xffffffffu, l, kFewRows);
             // A single item's slots fold their summaries of the same rows and
             // each writes half of the head dims, reading both slots' O (slot 1
             // has none when the share has one key tile).
@@ -707,7 +754,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             // each of the 32 rows a round: a store instruction then covers 8 rows
             // of 64 contiguous bytes, not 32 rows of 16.  16-byte pieces are
             // permuted by row against bank conflicts.
-            uint8_t* stage = sStage + (warp - 2) * 2048;
+            uint8_t* stage = sStage + (FEW ? t : (int)warp - 2) * 2048;
             const int dst = valid ? row : -1;
             const int c_begin = single ? t * (D / 2) : 0;
             auto put = [&](int q, const uint4& v) {   // piece q of this lane's row
@@ -743,6 +790,11 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     }
                 }
             };
+            // the P V of both terms of the row's probabilities (all lanes call it)
+            auto both_terms = [&](float x) {
+                return FEW ? x + __shfl_down_sync(0xffffffffu, x, kFewRows) : x;
+            };
+            auto zero_if_none = [&](float x) { return none ? 0.f : x; };
             // 64 accumulators at a time: of a two-tile item 64 columns of its own O,
             // of a single item 32 columns of both O
 #pragma unroll 1
@@ -760,14 +812,14 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     for (int c = 0; c < 32; ++c) {
                         float f = __uint_as_float(x0[c]) * s0;
                         if (with1) f = fmaf(__uint_as_float(x1[c]), s1, f);
-                        x0[c] = __float_as_uint(none ? 0.f : f);
+                        x0[c] = __float_as_uint(zero_if_none(both_terms(f)));
                     }
                     emit(x0, c_begin + 32 * pass);
                 } else {
 #pragma unroll
                     for (int c = 0; c < 32; ++c) {
-                        x0[c] = __float_as_uint(none ? 0.f : __uint_as_float(x0[c]) * s0);
-                        x1[c] = __float_as_uint(none ? 0.f : __uint_as_float(x1[c]) * s0);
+                        x0[c] = __float_as_uint(zero_if_none(both_terms(__uint_as_float(x0[c]) * s0)));
+                        x1[c] = __float_as_uint(zero_if_none(both_terms(__uint_as_float(x1[c]) * s0)));
                     }
                     emit(x0, 64 * pass);
                     emit(x1, 64 * pass + 32);

@@ -495,7 +495,10 @@ mea_status_t mea_paged_append(const void* q, void* q_out, const void* k, const v
  * device memory of at least mea_attn_paged_workspace_size bytes for the same
  * sizes and bounds on the current device (it depends on the SM count), 16-byte
  * aligned, scratch; two calls that may overlap on the GPU need one each.  The
- * same inputs give the same bits.  Errors: MEA_ERR_INVALID_ARG,
+ * same inputs give the same bits.  bf16: with at most 16 rows per key/value head
+ * and sequence (H / H_kv heads times max_q tokens) the probabilities enter the sum
+ * over v_j with an error of at most 2^-16 of each; with more they are rounded to
+ * bf16, 2^-8 of each, as in mea_attn_fwd.  Sums are fp32.  Errors: MEA_ERR_INVALID_ARG,
  * MEA_ERR_UNSUPPORTED, MEA_ERR_MISALIGNED, MEA_ERR_WORKSPACE, MEA_ERR_CUDA.
  */
 mea_status_t mea_attn_paged_workspace_size(int T, int B, int H, int H_kv, int D, int max_q, int max_kv,
