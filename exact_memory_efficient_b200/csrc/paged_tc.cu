@@ -648,11 +648,14 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 float mx = fmaxf(fmax3(mxa[0], mxa[1], mxa[2]), fmax3(fmax3(mxa[3], mxa[4], mxa[5]), mxa[6], mxa[7]));
                 if constexpr (FEW) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, kFewRows));
                 const float m_blk = fmaxf(mx * c_log2, kNoKey);
+                // Only the sequence's rows say when the warp's references move: the others
+                // hold other sequences' tokens or what ran before, and a move out of turn
+                // rounds the rows' probabilities to other bits.  A row and its copy agree.
                 float alpha = 1.f;
                 bool rescale = false;
                 if (it == 0) {
                     m_ref = m_blk;
-                } else if (__any_sync(0xffffffffu, m_blk - m_ref > kRescaleThreshold)) {
+                } else if (__any_sync(0xffffffffu, valid && m_blk - m_ref > kRescaleThreshold)) {
                     const float m_new = fmaxf(m_ref, m_blk);
                     alpha = ex2_approx(m_ref - m_new);
                     m_ref = m_new;
