@@ -5,7 +5,7 @@
 // brought into range before it is used as an index, and a value that was out
 // of range is recorded in the per-device error word (MEA_DEVERR_PAGE): a bad
 // table costs wrong results for its sequence, never an access outside the
-// caller's buffers.
+// caller's buffers, and never a write to a page that the table does not name.
 #pragma once
 
 #include <cstdint>
@@ -40,12 +40,17 @@ __device__ __forceinline__ Seq load_seq(const PagedBatch& s, int b) {
 __device__ __forceinline__ int page_entry(const PagedBatch& s, int b, int i) {
     return s.page_table[(size_t)b * s.max_pages + i];
 }
-__device__ __forceinline__ int page_of(const PagedBatch& s, int entry) {
+__device__ __forceinline__ int page_of(const PagedBatch& s, int entry, int otherwise = 0) {
     if ((unsigned)entry < (unsigned)s.num_pages) return entry;
     flag_bad_page();
-    return 0;
+    return otherwise;
 }
+// For reads: an entry out of range reads page 0.
 __device__ __forceinline__ int load_page(const PagedBatch& s, int b, int i) { return page_of(s, page_entry(s, b, i)); }
+// For writes: an entry out of range is -1 and nothing is written (page 0 is another sequence's).
+__device__ __forceinline__ int page_to_write(const PagedBatch& s, int b, int i) {
+    return page_of(s, page_entry(s, b, i), -1);
+}
 
 // A tile of 128 keys of bf16 pages in shared memory, as one TMA box per page
 // lays it out: groups of 8 keys, in a group the blocks of 64 head dims, in a

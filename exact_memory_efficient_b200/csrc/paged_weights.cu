@@ -107,8 +107,8 @@ __global__ void __launch_bounds__(kThreads) paged_weights_kernel(const PagedWeig
             const int j = 4 * ty + i;
             if (tx == 0 && j < keys) {
                 const int key = k0 + j;
-                const size_t row = (((size_t)load_page(a.s, b, key >> a.s.page_shift) * a.Hkv + kvh) << a.s.page_shift) + (key & mask);
-                a.weights[row] += sum[i];
+                const int page = page_to_write(a.s, b, key >> a.s.page_shift);
+                if (page >= 0) a.weights[(((size_t)page * a.Hkv + kvh) << a.s.page_shift) + (key & mask)] += sum[i];
             }
         }
     }

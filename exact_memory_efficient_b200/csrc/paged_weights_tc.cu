@@ -200,9 +200,9 @@ __device__ __forceinline__ void add_pair(float& d0, float& d1, float x0, float x
         : "f"(x0), "f"(x1));
 }
 
-// Slot of key `key` of (b, h) in weights.
-__device__ __forceinline__ size_t weight_at(const PagedBatch& s, int Hkv, int b, int h, int key) {
-    return (((size_t)load_page(s, b, key >> s.page_shift) * Hkv + h) << s.page_shift) + (key & ((1 << s.page_shift) - 1));
+// Slot of key `key` of head h in weights, in page `page`.
+__device__ __forceinline__ size_t weight_at(const PagedBatch& s, int Hkv, int page, int h, int key) {
+    return (((size_t)page * Hkv + h) << s.page_shift) + (key & ((1 << s.page_shift) - 1));
 }
 
 template <int D, bool FEW>
@@ -431,7 +431,7 @@ paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             const bool whole = w.whole();
             // the key's page, looked up while the tiles arrive and not used before the end
             const bool mine = half == 0 && key < w.sq.L;
-            const int page = mine && whole ? load_page(a.s, w.b, key >> a.s.page_shift) : 0;
+            const int page = mine && whole ? page_to_write(a.s, w.b, key >> a.s.page_shift) : -1;
             const int f = first_tile(w.sq, tt, w.i);
             const int seen = w.sq.L - w.sq.n;
             float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -509,11 +509,10 @@ paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             }
             if (!whole) {
                 a.part_sum[(size_t)(2 * blockIdx.x + (w.first ? 0 : 1)) * 2 * kTile + t * kTile + r] = total;
-            } else if (mine) {
+            } else if (page >= 0) {
                 // one addition per slot and call, so its order cannot matter: a
                 // reduction that nothing waits for (old + total, rounded once)
-                atomicAdd(&a.weights[(((size_t)page * a.Hkv + w.h) << a.s.page_shift) + (key & ((1 << a.s.page_shift) - 1))],
-                          total);
+                atomicAdd(&a.weights[weight_at(a.s, a.Hkv, page, w.h, key)], total);
             }
         }
     }
@@ -575,7 +574,8 @@ __global__ void __launch_bounds__(2 * kTile) weights_merge_kernel(const PagedWei
             sum += x[3];
         }
     }
-    if (key < sq.L) a.weights[weight_at(a.s, a.Hkv, p.b, p.h, key)] += sum;
+    const int page = key < sq.L ? page_to_write(a.s, p.b, key >> a.s.page_shift) : -1;
+    if (page >= 0) a.weights[weight_at(a.s, a.Hkv, page, p.h, key)] += sum;
 }
 
 template <int D, bool FEW>

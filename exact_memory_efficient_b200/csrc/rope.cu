@@ -195,7 +195,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a, in
     int slot = 0;
     // the token's sequence and, for a key or value, its slot: the offset of head 0
     // in the cache, or -1 (rows outside every sequence stay as they were; with
-    // more new tokens than keys the first ones have no slot)
+    // more new tokens than keys the first ones have no slot; a page table entry
+    // out of range names none)
     auto locate = [&](bool cached) -> long long {
         const int b = find_row(a.s, tok);
         if (b < 0) return -1;
@@ -205,8 +206,9 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a, in
         slot = sq.L - sq.n + (tok - sq.q0);
         if (!cached) return 0;
         if (slot < 0) return -1;
-        const long long first = (long long)load_page(a.s, b, slot >> a.s.page_shift) * a.Hkv;
-        return first * page_heads + (slot & ((1 << a.s.page_shift) - 1));
+        const int page = page_to_write(a.s, b, slot >> a.s.page_shift);
+        if (page < 0) return -1;
+        return (long long)page * a.Hkv * page_heads + (slot & ((1 << a.s.page_shift) - 1));
     };
     auto turn = [&](Turn<T, INTER>& t) {
         t.load(a.freq, unit, a.positions ? a.positions[tok] : slot, a.mscale, false);

@@ -426,8 +426,9 @@ mea_status_t mea_attn_bwd_noalloc(const void* q, const void* k, const void* v,
  *  - cu_q, kv_len and page_table are device memory and cannot be checked when
  *    the call is made.  A value out of range makes the results of its sequence
  *    (with offsets that run backwards: of the call) undefined, but no access
- *    leaves the buffers given here; mea_last_device_error() then reports
- *    MEA_ERR_PAGE.
+ *    leaves the buffers given here, and keys, values and weights whose page
+ *    entry is out of range are not written anywhere; mea_last_device_error()
+ *    then reports MEA_ERR_PAGE.
  *  - dtype, head dims, ownership, streams and errors as above: bf16 with D 64
  *    or 128, fp32 with D 32, 64, 96 or 128.  T == 0 or B == 0 is a no-op.
  *  - B and H_kv are at most 65535.
