@@ -426,7 +426,8 @@ mea_status_t mea_paged_evict(void* k_cache, void* v_cache, float* weights, const
     if (n_keep < 1 || n_recent < 0 || n_recent > n_keep) return invalid(where, "0 <= n_recent <= n_keep, 1 <= n_keep");
     if (dst_max_pages < 0) return invalid(where, "negative size");
     if ((long long)B * H_kv > 65535) return api_fail(MEA_ERR_UNSUPPORTED, where, "B * H_kv above 65535");
-    if ((long long)B * H_kv * n_keep > 0x7fffffffLL) return invalid(where, "B * H_kv * n_keep too large");
+    // slots are counted in ints, up to one batch of the kernels (a few thousand) beyond the last
+    if ((long long)B * H_kv * n_keep > 0x7fffffffLL - 65536) return invalid(where, "B * H_kv * n_keep too large");
     if (B == 0) return MEA_OK;
     if (!k_cache || !v_cache || !weights || !page_table || !kv_len || !dst_table || !keep_idx)
         return invalid(where, "null pointer");

@@ -220,7 +220,7 @@ constexpr int kMoveDepth = 2;
 __device__ __forceinline__ void write_length(const EvictArgs& a, int b, const int* idx) {
     int n = 0, hi = a.n_keep;   // first j with idx[j] < 0; every head keeps the same number
     while (n < hi) {
-        const int mid = (n + hi) >> 1;
+        const int mid = n + ((hi - n) >> 1);
         if (idx[mid] >= 0) n = mid + 1;
         else hi = mid;
     }
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
     const int* idx = a.keep_idx + (size_t)blockIdx.y * a.n_keep;
     const int l = (int)threadIdx.x % lanes;
     const int groups = kMoveThreads / lanes;
-    const int j1 = min(a.n_keep, ((int)blockIdx.x + 1) * per_cta);
+    const int j1 = (int)min((long long)a.n_keep, ((long long)blockIdx.x + 1) * per_cta);
     if ((int)threadIdx.x < groups * lanes) {
         for (int j0 = (int)blockIdx.x * per_cta + (int)threadIdx.x / lanes; j0 < j1; j0 += kMoveDepth * groups) {
             int from[kMoveDepth];

@@ -547,7 +547,7 @@ mea_status_t mea_attn_paged_weights(const void* q, const float* lse, const void*
  * not written and reported as MEA_ERR_PAGE.
  * No two sequences may share a destination page.  Keys keep the rotation of
  * their original positions.  0 <= n_recent <= n_keep, 1 <= n_keep;
- * B * H_kv <= 65535.  Errors: MEA_ERR_INVALID_ARG, MEA_ERR_UNSUPPORTED,
+ * B * H_kv <= 65535, B * H_kv * n_keep <= 2^31 - 65537.  Errors: MEA_ERR_INVALID_ARG, MEA_ERR_UNSUPPORTED,
  * MEA_ERR_MISALIGNED, MEA_ERR_CUDA.
  */
 mea_status_t mea_paged_evict(void* k_cache, void* v_cache, float* weights, const int* page_table, const int* kv_len,
