@@ -432,12 +432,16 @@ paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             // the key's page, looked up while the tiles arrive and not used before the end
             const bool mine = half == 0 && key < w.sq.L;
             const int page = mine && whole ? page_to_write(a.s, w.b, key >> a.s.page_shift) : -1;
+            [[maybe_unused]] float old = 0.f;
             const int f = first_tile(w.sq, tt, w.i);
             const int seen = w.sq.L - w.sq.n;
             float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
             for (int u = w.u0; u < w.u1; ++u, ++qc) {
                 const int s = qc % C::kQStages;
                 if (!(ok = wait_all(&bars->q_full[s], (qc / C::kQStages) & 1))) break;
+                // decode, an item a unit: the weight before, asked for ahead of the wait for the scores
+                if constexpr (FEW)
+                    if (u == w.u0 && page >= 0) old = a.weights[weight_at(a.s, a.Hkv, page, w.h, key)];
                 if (!work) {
                     mbar_arrive(&bars->q_empty[s]);
                     continue;
@@ -510,9 +514,10 @@ paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             if (!whole) {
                 a.part_sum[(size_t)(2 * blockIdx.x + (w.first ? 0 : 1)) * 2 * kTile + t * kTile + r] = total;
             } else if (page >= 0) {
-                // one addition per slot and call, so its order cannot matter: a
-                // reduction that nothing waits for (old + total, rounded once)
-                atomicAdd(&a.weights[weight_at(a.s, a.Hkv, page, w.h, key)], total);
+                // One addition per slot and call, by this thread alone.  (A global fp32
+                // atomic would flush subnormal sums, which the merge of parts keeps.)
+                float& slot = a.weights[weight_at(a.s, a.Hkv, page, w.h, key)];
+                slot = (FEW ? old : slot) + total;
             }
         }
     }

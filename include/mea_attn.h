@@ -514,9 +514,10 @@ mea_status_t mea_attn_paged(const void* q, const void* k_cache, const void* v_ca
 /*
  * weights_j += sum over the rows i of the call's query heads of the key's group
  * that see key j of exp(scale * q_i . k_j - lse_i), with lse [T, H] from
- * mea_attn_paged of the same call: what key j contributed.  The sums have a
- * fixed order (no atomics): the same inputs give the same bits.  workspace: as
- * for mea_attn_paged, of mea_attn_paged_weights_workspace_size bytes.
+ * mea_attn_paged of the same call: what key j contributed.  Every slot
+ * receives one addition per call, of a sum in a fixed order: the same inputs give
+ * the same bits.  workspace: as for mea_attn_paged, of
+ * mea_attn_paged_weights_workspace_size bytes.
  * Two sequences of a call must not share a page here (each would add to the
  * same sums).  Errors: MEA_ERR_INVALID_ARG, MEA_ERR_UNSUPPORTED,
  * MEA_ERR_MISALIGNED, MEA_ERR_WORKSPACE, MEA_ERR_CUDA.
