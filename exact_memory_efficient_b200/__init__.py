@@ -485,7 +485,10 @@ def load_binding():
     if _BINDING is not None:
         return _BINDING
     load_library()
+    from . import build
     try:
+        if not build.binding_fits():
+            raise ImportError(f"no {build.binding_tag()}")
         from . import _binding
     except ImportError as e:
         raise RuntimeError(

@@ -20,6 +20,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
@@ -72,17 +73,31 @@ def _compile(nvcc: str, src: str, verbose: bool, extra: list[str]) -> str:
     return obj
 
 
+def binding_tag() -> str:
+    """The Python and torch of this interpreter, as text that a binding built for them holds."""
+    import torch
+    return (f"_binding for {sysconfig.get_config_var('SOABI')}, torch {torch.__version__} {torch.version.git_version}, "
+            f"cxx11 abi {int(torch._C._GLIBCXX_USE_CXX11_ABI)}")
+
+
+def binding_fits() -> bool:
+    """Whether _binding.so was built for this interpreter (found in the file: one of another ABI cannot be asked)."""
+    try:
+        with open(BINDING_PATH, "rb") as f:
+            return binding_tag().encode() + b"\0" in f.read()
+    except FileNotFoundError:
+        return False
+
+
 def needs_binding() -> bool:
     src = max(os.path.getmtime(f) for f in (BINDING_SRC, os.path.join(INCLUDE, "mea_attn.h"), os.path.abspath(__file__)))
-    return not os.path.exists(BINDING_PATH) or os.path.getmtime(BINDING_PATH) < src
+    return not binding_fits() or os.path.getmtime(BINDING_PATH) < src
 
 
 def build_binding(force: bool = False, verbose: bool = False) -> str:
     """Compile _binding.so (needs the library)."""
     if not force and not needs_binding():
         return BINDING_PATH
-    import sysconfig
-
     import torch
     torch_dir = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc_path()))
@@ -90,7 +105,7 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
                 sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE]
     tmp = BINDING_PATH + ".tmp"
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DMEA_BINDING_FOR="{binding_tag()}"',
            *[x for p in includes for x in ("-isystem" if p != INCLUDE else "-I", p)], BINDING_SRC, "-o", tmp,
            "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
            "-L", PKG_DIR, f"-l:{LIB_NAME}", "-Wl,-rpath,$ORIGIN"]

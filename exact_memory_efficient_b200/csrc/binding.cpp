@@ -481,4 +481,9 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, g_method
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&g_module); }
+PyMODINIT_FUNC PyInit__binding() {
+    PyObject* m = PyModule_Create(&g_module);
+    // the Python and torch that this was compiled against (build.py looks for the text in the file)
+    if (m != nullptr && PyModule_AddStringConstant(m, "built_for", MEA_BINDING_FOR) != 0) Py_CLEAR(m);
+    return m;
+}
