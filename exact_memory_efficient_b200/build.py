@@ -9,7 +9,8 @@ kernels).  The CUDA runtime is linked statically.
 
 _binding.so beside it is the CPython binding of the rotary and paged-cache
 entry points for torch tensors (csrc/binding.cpp), compiled against the torch
-and Python of the running interpreter and linked to the library.
+and Python of the running interpreter and linked to the library.  It needs g++
+and their headers; without them the library is built alone.
 """
 
 from __future__ import annotations
@@ -94,17 +95,32 @@ def needs_binding() -> bool:
     return not binding_fits() or os.path.getmtime(BINDING_PATH) < src
 
 
+def binding_lacks() -> list[str]:
+    """What is not installed of what _binding.so needs beside the library."""
+    try:
+        import torch
+    except ImportError:
+        return ["torch"]
+    headers = {"Python.h": sysconfig.get_paths()["include"],
+               "ATen/ATen.h": os.path.join(os.path.dirname(torch.__file__), "include")}
+    return [h for h, at in headers.items() if not os.path.exists(os.path.join(at, h))] + \
+        ([] if shutil.which("g++") else ["g++"])
+
+
 def build_binding(force: bool = False, verbose: bool = False) -> str:
     """Compile _binding.so (needs the library)."""
     if not force and not needs_binding():
         return BINDING_PATH
+    lacks = binding_lacks()
+    if lacks:
+        raise RuntimeError(f"_binding.so needs {', '.join(lacks)}")
     import torch
     torch_dir = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc_path()))
     includes = [os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
                 sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE]
     tmp = BINDING_PATH + ".tmp"
-    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+    cmd = [shutil.which("g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DMEA_BINDING_FOR="{binding_tag()}"',
            *[x for p in includes for x in ("-isystem" if p != INCLUDE else "-I", p)], BINDING_SRC, "-o", tmp,
            "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
@@ -121,8 +137,14 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
 
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
+    """The library, and the binding where what it needs is installed (the library needs nvcc alone)."""
     _build_library(force, verbose, extra)
-    build_binding(force, verbose)
+    lacks = binding_lacks()
+    if lacks and ("torch" in lacks or force or needs_binding()):
+        sys.stderr.write(f"_binding.so is not built without {', '.join(lacks)}: the rotary and paged-cache functions of "
+                         "the Python package need it\n")
+    elif not lacks:
+        build_binding(force, verbose)
     return LIB_PATH
 
 

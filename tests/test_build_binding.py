@@ -35,3 +35,30 @@ def test_a_rebuilt_binding_fits(monkeypatch, tmp_path):
     assert b.needs_binding()
     b.build_binding()
     assert not b.needs_binding()
+
+
+def without_python_headers(monkeypatch, tmp_path):
+    monkeypatch.setattr(b, "BINDING_PATH", str(tmp_path / "_binding.so"))
+    monkeypatch.setattr(b.sysconfig, "get_paths", lambda: {"include": str(tmp_path)})
+
+
+def test_the_library_is_built_where_the_binding_cannot_be(monkeypatch, tmp_path, capfd):
+    """The C library needs nvcc alone; what the binding lacks is said, and load_binding() still fails loudly."""
+    without_python_headers(monkeypatch, tmp_path)
+    assert b.build() == b.LIB_PATH
+    said = capfd.readouterr().err
+    assert "_binding.so" in said and "Python.h" in said
+    with pytest.raises(RuntimeError, match="Python.h"):
+        b.build_binding()
+    monkeypatch.setattr(m, "_BINDING", None)
+    with pytest.raises(RuntimeError, match="there is no fallback"):
+        m.load_binding()
+
+
+def test_each_thing_that_the_binding_needs(monkeypatch):
+    assert b.binding_lacks() == []
+    monkeypatch.setattr(b.shutil, "which", lambda name: None if name == "g++" else "/usr/bin/" + name)
+    assert b.binding_lacks() == ["g++"]
+    monkeypatch.undo()
+    monkeypatch.setitem(__import__("sys").modules, "torch", None)      # import torch raises ImportError
+    assert b.binding_lacks() == ["torch"]
