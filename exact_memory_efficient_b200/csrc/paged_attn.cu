@@ -465,7 +465,9 @@ cudaError_t launch_rows(const PagedAttnArgs& a, cudaStream_t stream) {
 
 template <typename T, int DPL>
 cudaError_t dispatch_rows(const PagedAttnArgs& a, cudaStream_t stream) {
-    switch (a.rows) {
+    // bf16 comes here with groups above 128 heads alone: always eight rows
+    if constexpr (sizeof(T) == 2) return launch_rows<T, DPL, 8>(a, stream);
+    else switch (a.rows) {
         case 1: return launch_rows<T, DPL, 1>(a, stream);
         case 2: return launch_rows<T, DPL, 2>(a, stream);
         case 4: return launch_rows<T, DPL, 4>(a, stream);
@@ -475,6 +477,7 @@ cudaError_t dispatch_rows(const PagedAttnArgs& a, cudaStream_t stream) {
 
 template <typename T, int DPL>
 int blocks_rows(int rows) {
+    if constexpr (sizeof(T) == 2) return Cfg<T, DPL, 8>::kMinBlocks;
     return rows <= 1 ? Cfg<T, DPL, 1>::kMinBlocks : rows <= 2 ? Cfg<T, DPL, 2>::kMinBlocks
          : rows <= 4 ? Cfg<T, DPL, 4>::kMinBlocks : Cfg<T, DPL, 8>::kMinBlocks;
 }
