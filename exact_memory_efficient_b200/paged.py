@@ -127,7 +127,7 @@ class PagedCache:
         before = [(s, len(self._pages[s]), self._len[s], self._pos[s]) for s in seqs]
         try:
             return self._step(q, k, v, seqs, counts, need, scale)
-        except Exception:   # a refused call leaves the page list as it was
+        except BaseException:   # a refused or interrupted call leaves the page list as it was
             for s, held, length, pos in before:
                 self._free.extend(reversed(self._pages[s][held:]))
                 del self._pages[s][held:]
