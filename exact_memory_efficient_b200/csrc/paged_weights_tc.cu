@@ -38,6 +38,7 @@ namespace {
 
 constexpr int kTile = 128;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr unsigned long long kUnitLimitNs = 16000;   // of a unit, some ten times what it takes at low clocks
 
 // FEW: at most kFewRows rows per query tile (decode).  Q then takes 2 KB per 64
 // head dims and the space goes to K: three pairs in flight instead of two at
@@ -278,8 +279,12 @@ paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         const int outside = a.s.num_pages * a.Hkv;
         int li = 0;                 // items asked for
         bool ok = true;
+        // K comes an item ahead, and a pair is free when all units of its item are
+        // done: about 1 us each, so that a million query tiles take the whole limit
+        // of a wait.  It grows with the longest item so far.
+        int longest = 0;
         auto wait = [&](uint64_t* bar, unsigned parity) -> bool {
-            const int got = lane != 0 || mbar_wait(bar, parity, abort_flag);
+            const int got = lane != 0 || mbar_wait(bar, parity, abort_flag, kWaitLimitNs + longest * kUnitLimitNs);
             return __shfl_sync(0xffffffffu, got, 0) != 0;
         };
         // page coordinates of the lane's boxes in an item's two key tiles, looked up
@@ -319,6 +324,7 @@ paged_weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                                 &bars->k_full[ks], 0, 0, 0,
                                 (((2 * w.i + 1) * kTile + my_row) & ((1 << shift) - 1)) >> 3, z[1]);
             }
+            longest = max(longest, w.u1 - w.u0);
             Walk ahead = w;
             ahead.next(a);
             if (!ahead.done()) look_up(ahead, z_next);

@@ -85,16 +85,17 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, unsigned parity) {
 
 // Bounded wait for the phase with the given parity to complete.  `abort` (in
 // shared memory) is polled so that once any thread of the CTA has given up,
-// the others stop waiting too.  Returns false on timeout or abort.
-__device__ __forceinline__ bool mbar_wait(uint64_t* bar, unsigned parity,
-                                          volatile int* abort_flag) {
+// the others stop waiting too.  Returns false on timeout or abort.  limit_ns: for
+// a wait that lasts as long as an amount of work, more than the usual limit.
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, unsigned parity, volatile int* abort_flag,
+                                          unsigned long long limit_ns = kWaitLimitNs) {
     if (mbar_try_wait(bar, parity)) return true;
     const unsigned long long t0 = globaltimer_ns();
     for (unsigned it = 1;; ++it) {
         if (mbar_try_wait(bar, parity)) return true;
         if ((it & 63u) == 0) {
             if (abort_flag != nullptr && *abort_flag) return false;
-            if (globaltimer_ns() - t0 > kWaitLimitNs) {
+            if (globaltimer_ns() - t0 > limit_ns) {
                 flag_timeout();
                 if (abort_flag != nullptr) *abort_flag = 1;
                 return false;
