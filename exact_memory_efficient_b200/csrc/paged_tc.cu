@@ -79,8 +79,9 @@ constexpr unsigned kIdescNegateA = 1u << 13;
 // The terms are two rows of the same MMA: Q is loaded twice, 16 rows apart, the
 // lanes of a row and of its copy have the same S, form 32 of every 64 probabilities
 // each and exchange the terms; the two rows of O are added at the item's end (ragged
-// decode of 16 over 8191 keys, 32 over 8 heads: 65.2 us with one term, 64.7 so; with
-// every lane on all of its row's columns 74.5, and as a second MMA 82).
+// decode of 16 over 500 to 8191 keys, 32 over 8 heads: 65.9 us with one term, 64.2
+// so; 64 over 300 to 2000 keys, 3.5 item ends a CTA: 82.0 and 83.6.  With every lane
+// on all of its row's columns the first takes 74.5, as a second MMA 82).
 // Larger tiles have no rows to spare: there P is rounded to bf16 once, at most 2^-8 p
 // of each value with either sign, as in the forward kernels; a second MMA for the
 // rest takes 3 chunks of 97 to 250 tokens over 16384 keys from 158 to 218 us, 4
@@ -96,7 +97,7 @@ struct Cfg {
     static constexpr int kStages = D == 64 ? (FEW ? 8 : 6) : (FEW ? 6 : 4);
     static constexpr int kSmemData = (2 * kQBytes + kStages * kTileBytes + 1023) / 1024 * 1024;
     static constexpr int kMergeBytes = 2 * kTile * 2 * 4;   // both slots' (m, l) per row
-    static constexpr int kStageBytes = (FEW ? 2 : 8) * 2048;   // epilogue: 32 rows x 64 bytes per warp with rows
+    static constexpr int kStageBytes = FEW ? 2 * 4096 : 8 * 2048;   // epilogue: 32 rows x 128 or 64 bytes per warp
     static constexpr int kSmemBytes = kSmemData + kMergeBytes + kStageBytes + 1024 /*barriers*/ + 1024 /*alignment*/;
     static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
@@ -753,11 +754,14 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             const float s0 = w0 * inv, s1 = w1 * inv;
             const int row = whole ? (w.q0 + tok) * a.H + w.h * G + g_r
                                   : (2 * w.part + (single ? 0 : t)) * tt * G + r;
-            // Rows go out through the warp's 2 KB of shared memory, 64 bytes of
+            // Rows go out through the warp's part of shared memory, 64 bytes of
             // each of the 32 rows a round: a store instruction then covers 8 rows
             // of 64 contiguous bytes, not 32 rows of 16.  16-byte pieces are
-            // permuted by row against bank conflicts.
-            uint8_t* stage = sStage + (FEW ? t : (int)warp - 2) * 2048;
+            // permuted by row against bank conflicts.  With few rows a round is 32
+            // fp32 columns, and a row and its copy, the two terms' P V, are added on
+            // the way (64 x 2000 keys, 32 over 8 heads: 83.6 us; with a shuffle per column
+            // in the registers 85.7).
+            uint8_t* stage = sStage + (FEW ? t * 4096 : ((int)warp - 2) * 2048);
             const int dst = valid ? row : -1;
             const int c_begin = single ? t * (D / 2) : 0;
             auto put = [&](int q, const uint4& v) {   // piece q of this lane's row
@@ -775,7 +779,29 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 __syncwarp();
             };
             auto emit = [&](const uint32_t (&x)[32], int col) {   // 32 columns of the warp's rows
-                if (whole) {
+                if constexpr (FEW) {
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        *reinterpret_cast<uint4*>(stage + lane * 128 + ((q ^ (lane & 7)) * 16)) =
+                            make_uint4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < kFewRows / 4; ++i) {
+                        const int rr = 4 * i + (int)lane / 8, q = (int)lane % 8;
+                        const int d = __shfl_sync(0xffffffffu, dst, rr);
+                        const uint8_t* piece = stage + rr * 128 + ((q ^ (rr & 7)) * 16);
+                        float4 v = *reinterpret_cast<const float4*>(piece);
+                        const float4 w2 = *reinterpret_cast<const float4*>(piece + kFewRows * 128);
+                        v = make_float4(v.x + w2.x, v.y + w2.y, v.z + w2.z, v.w + w2.w);
+                        if (d < 0) continue;
+                        if (whole)
+                            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + (size_t)d * D + col + 4 * q) =
+                                make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+                        else
+                            *reinterpret_cast<float4*>(a.part_acc + (size_t)d * D + col + 4 * q) = v;
+                    }
+                    __syncwarp();
+                } else if (whole) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
                         put(q, make_uint4(pack_bf16x2(__uint_as_float(x[8 * q]), __uint_as_float(x[8 * q + 1])),
@@ -793,11 +819,6 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     }
                 }
             };
-            // the P V of both terms of the row's probabilities (all lanes call it)
-            auto both_terms = [&](float x) {
-                return FEW ? x + __shfl_down_sync(0xffffffffu, x, kFewRows) : x;
-            };
-            auto zero_if_none = [&](float x) { return none ? 0.f : x; };
             // 64 accumulators at a time: of a two-tile item 64 columns of its own O,
             // of a single item 32 columns of both O
 #pragma unroll 1
@@ -815,14 +836,14 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     for (int c = 0; c < 32; ++c) {
                         float f = __uint_as_float(x0[c]) * s0;
                         if (with1) f = fmaf(__uint_as_float(x1[c]), s1, f);
-                        x0[c] = __float_as_uint(zero_if_none(both_terms(f)));
+                        x0[c] = __float_as_uint(none ? 0.f : f);
                     }
                     emit(x0, c_begin + 32 * pass);
                 } else {
 #pragma unroll
                     for (int c = 0; c < 32; ++c) {
-                        x0[c] = __float_as_uint(zero_if_none(both_terms(__uint_as_float(x0[c]) * s0)));
-                        x1[c] = __float_as_uint(zero_if_none(both_terms(__uint_as_float(x1[c]) * s0)));
+                        x0[c] = __float_as_uint(none ? 0.f : __uint_as_float(x0[c]) * s0);
+                        x1[c] = __float_as_uint(none ? 0.f : __uint_as_float(x1[c]) * s0);
                     }
                     emit(x0, 64 * pass);
                     emit(x1, 64 * pass + 32);
