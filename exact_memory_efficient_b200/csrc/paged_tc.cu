@@ -499,9 +499,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                             if (j == 0 && !(ok = o_is_free(0))) break;
                             if (!(ok = pv_halves(0, cnt0 & 1, v_off, acc0))) break;
                             ++cnt0;
-                            // slot 0 has handed over a P of this item: no wait, but ahead of its o_final
-                            if (j == 0 && !(ok = o_is_free(1))) break;
-                            if (j == n0 - 1) mma_commit(&bars->o_final[0]);
+                            if (j == n0 - 1 && j > 0) mma_commit(&bars->o_final[0]);
                         }
                         if (more) {
                             if (!(ok = next_tile(k_off, k_stage))) break;
@@ -511,7 +509,12 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                                 mma_commit(&bars->s_full[0]);
                             }
                         }
-                        if (j == 0 && n0 == 0 && !(ok = o_is_free(1))) break;   // slot 0's o_final is the item's end
+                        if (j == 0) {
+                            // Behind the next S, where it delays nothing (ahead of it 4 prompts
+                            // take 323 us, here 313); a slot 0 of one key tile is let go after it.
+                            if (!(ok = o_is_free(1))) break;
+                            if (n0 == 1) mma_commit(&bars->o_final[0]);
+                        }
                         if (!(ok = pv_halves(1, cnt1 & 1, v_off, acc0))) break;
                         ++cnt1;
                         mma_commit(&bars->empty[v_stage]);
