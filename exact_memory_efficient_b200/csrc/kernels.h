@@ -219,7 +219,6 @@ cudaError_t launch_paged_merge(const PagedAttnArgs& a, bool bf16, cudaStream_t s
 // {D, H, T} with box {64, G, tt}; k, v as PageTile (paged.cuh) has them.
 // Workspace: two parts per CTA of up to 2 * tt * G rows each: part_acc [2 sm_count,
 // rows, D], part_ml [2 sm_count, rows, 2], parts [2 sm_count].
-// 2 * tt * G rows: part_acc [2 sm_count, rows, D], part_ml [.., 2], parts [2 sm_count].
 struct PagedPart {
     int b, h, i, t0, t1, n_kv;   // key tiles [t0, t1) of item i of (b, h); n_kv = 0: none
     int q0, n;                   // the sequence's packed rows

@@ -107,11 +107,6 @@ __device__ __forceinline__ int find_row(const PagedBatch& s, int t) {
     return lo;
 }
 
-// The costs of all sequences as one line: calls locate(b, before, cost, W) for
-// every b, with the sum of the costs in front of b and of all.  All THREADS
-// threads of the block call it; a thread's cost(b) and locate(b, ...) calls
-// follow one another, so that cost() may leave what locate() needs.  What locate()
-// writes is seen after the block's next barrier.
 // x / y, and the border of share i of n, of sizes that most often fit 32 bits (a
 // division of 64-bit numbers takes some 150 cycles, and shares are found before any work)
 __device__ __forceinline__ long long divide(long long x, long long y) {
@@ -119,6 +114,11 @@ __device__ __forceinline__ long long divide(long long x, long long y) {
 }
 __device__ __forceinline__ long long share_begin(long long W, unsigned i, unsigned n) { return divide(W * i, n); }
 
+// The costs of all sequences as one line: calls locate(b, before, cost, W) for
+// every b, with the sum of the costs in front of b and of all.  All THREADS
+// threads of the block call it; a thread's cost(b) and locate(b, ...) calls
+// follow one another, so that cost() may leave what locate() needs.  What locate()
+// writes is seen after the block's next barrier.
 template <int THREADS, typename Cost, typename Locate>
 __device__ __forceinline__ void lay_out_costs(int B, long long (&warp_sum)[THREADS / 32], Cost&& cost, Locate&& locate) {
     const int tid = (int)threadIdx.x;

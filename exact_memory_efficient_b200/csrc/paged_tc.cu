@@ -38,7 +38,7 @@
 // per row at 16 per clock and SM, and their issue) -> P V -> next S, about 3,550
 // cycles per key tile of an item against 2,048 of MMAs, at the clock that the 1 kW
 // power limit leaves (1.5-1.8 GHz): 2048 tokens over 16384 keys of 16 heads
-// (D = 128) take 255 us, 1010 TFLOP/s.  A slot that waits for the other's softmax
+// (D = 128) take 260 us, 990 TFLOP/s.  A slot that waits for the other's softmax
 // before its first S, or before every S, is not faster (264 and 298 us when this
 // took 263); exponentials on the FMA pipe are slower with every share tried (one
 // pair in eight: 11% for 4 prompts): issue, not the exponential unit, binds.  With
