@@ -21,6 +21,9 @@
 // others, whose sums are added at the item's end (four warps with few rows).
 // TMEM: two score buffers of 128 columns per key tile.
 //
+// Rounding: exp2 is the approximate instruction (2^-22 relative), sums are fp32, 16
+// running ones per key (8 with few rows) and their sum at the item's end.
+//
 // Bound: decode reads K once (HBM); with many rows one exponential per score
 // binds (16 per clock and SM), the tensor cores need half that time.  With four
 // warps per key tile every warp waited for the same barriers at the same time

@@ -516,9 +516,9 @@ mea_status_t mea_attn_paged(const void* q, const void* k_cache, const void* v_ca
  * that see key j of exp(scale * q_i . k_j - lse_i), with lse [T, H] from
  * mea_attn_paged of the same call: what key j contributed.  Every slot
  * receives one addition per call, of a sum in a fixed order: the same inputs give
- * the same bits.  workspace: as for mea_attn_paged, of
- * mea_attn_paged_weights_workspace_size bytes.
- * Two sequences of a call must not share a page here (each would add to the
+ * the same bits.  Sums are fp32: with n rows a relative error of up to n 2^-24.
+ * workspace: as for mea_attn_paged, of mea_attn_paged_weights_workspace_size
+ * bytes.  Two sequences of a call must not share a page here (each would add to the
  * same sums).  Errors: MEA_ERR_INVALID_ARG, MEA_ERR_UNSUPPORTED,
  * MEA_ERR_MISALIGNED, MEA_ERR_WORKSPACE, MEA_ERR_CUDA.
  */
