@@ -13,8 +13,7 @@
 // off the nearest whole number (exact), and only then rounded to fp32 for
 // sincospif: the error left is 2^-24 of half a turn plus 2^-52 of the
 // revolutions.  Sine and cosine, their products with mscale and those with x are
-// fp32, a rounding of 2^-24 each (an fp64 sine would cost more than the copy that
-// bounds the kernel); each result is rounded once to its type.
+// fp32, a rounding of 2^-24 each; each result is rounded once to its type.
 //
 // A thread owns one 16-byte vector of a head (two at the distance rot / 2 for
 // the half layout) of one token, forms its 2 to 8 sines and cosines once, and
